@@ -31,6 +31,8 @@ KPA_ERR_DEVICE_CHECK = 6
 KPA_F32 = 0
 KPA_BF16 = 1
 KPA_TOKEN_GROUP = 8
+KPA_PAGE_BF16 = 0
+KPA_PAGE_E4M3 = 1
 
 
 class kpa_config(ctypes.Structure):
@@ -38,6 +40,11 @@ class kpa_config(ctypes.Structure):
                 ("d2", ctypes.c_int32), ("r_q", ctypes.c_int32), ("r_k", ctypes.c_int32),
                 ("r_v", ctypes.c_int32), ("d_model", ctypes.c_int32), ("rope_base", ctypes.c_double),
                 ("dtype", ctypes.c_int), ("shared_b", ctypes.c_int32), ("order", ctypes.c_int32)]
+
+
+class kpa_pages(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("format", ctypes.c_int)]
 
 
 class KpaError(RuntimeError):
@@ -51,6 +58,7 @@ class KpaError(RuntimeError):
 
 _vp, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 _cfgp = ctypes.POINTER(kpa_config)
+_pgp = ctypes.POINTER(kpa_pages)
 _szp = ctypes.POINTER(ctypes.c_size_t)
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _SIGS = {
@@ -87,6 +95,15 @@ _SIGS = {
     "kpa_decode_lse": ([_cfgp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _f32, _vp, _vp, _vp, _sz, _vp],
                        ctypes.c_int),
     "kpa_merge_lse": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "kpa_paged_page_bytes": ([_cfgp, _pgp, _szp, _szp], ctypes.c_int),
+    "kpa_paged_append_factors": ([_cfgp, _pgp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "kpa_paged_read_factors": ([_cfgp, _pgp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "kpa_paged_prefill_workspace_size": ([_cfgp, _pgp, _i32, _i32, _i32, _i32, _i32, _szp], ctypes.c_int),
+    "kpa_paged_prefill": ([_cfgp, _pgp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp,
+                           _sz, _vp], ctypes.c_int),
+    "kpa_paged_decode_workspace_size": ([_cfgp, _pgp, _i32, _i32, _i32, _i32, _szp], ctypes.c_int),
+    "kpa_paged_decode": ([_cfgp, _pgp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp],
+                         ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -102,6 +119,15 @@ def make_config(shape, dtype: str = "bf16") -> kpa_config:
                       int(getattr(shape, "d_model", 0)), float(getattr(shape, "rope_base", 10000.0)),
                       KPA_BF16 if dtype == "bf16" else KPA_F32, int(getattr(shape, "shared_b", 0)),
                       int(getattr(shape, "order", 2)))
+
+
+_PAGE_FORMATS = {"bf16": KPA_PAGE_BF16, "e4m3": KPA_PAGE_E4M3}
+
+
+def make_pages(page_size: int, n_pages: int, table_stride: int, format: str = "bf16") -> kpa_pages:
+    """kpa_pages of a pool of n_pages pages of page_size slots ("bf16" or "e4m3"), indexed by
+    a page table of table_stride entries per sequence."""
+    return kpa_pages(int(page_size), int(n_pages), int(table_stride), _PAGE_FORMATS[format])
 
 
 def _addr(x):
@@ -301,6 +327,68 @@ def kpa_merge_lse(outs, lses, out, lse=None, stream=None):
                               _stream(stream)), "kpa_merge_lse")
 
 
+def kpa_paged_page_bytes(cfg, pages):
+    """(bytes of a page of the key plane, of the value plane)."""
+    k, v = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.kpa_paged_page_bytes(ctypes.byref(cfg), ctypes.byref(pages), ctypes.byref(k), ctypes.byref(v)),
+           "kpa_paged_page_bytes")
+    return k.value, v.value
+
+
+def kpa_paged_append_factors(cfg, pages, batch, n_rows, k_factors, v_factors, cu_rows, start_pos, page_table, kpool,
+                             vpool, stream=None):
+    """Write (and, for an e4m3 pool, quantise) the rows' factor records into their pages."""
+    _check(_lib.kpa_paged_append_factors(ctypes.byref(cfg), ctypes.byref(pages), batch, n_rows, _addr(k_factors),
+                                         _addr(v_factors), _addr(cu_rows), _addr(start_pos), _addr(page_table),
+                                         _addr(kpool), _addr(vpool), _stream(stream)), "kpa_paged_append_factors")
+
+
+def kpa_paged_read_factors(cfg, pages, batch, n_rows, cu_rows, start_pos, page_table, kpool, vpool, k_factors,
+                           v_factors, stream=None):
+    """Read the rows' records back as bf16 (keys as cached, with B rotated)."""
+    _check(_lib.kpa_paged_read_factors(ctypes.byref(cfg), ctypes.byref(pages), batch, n_rows, _addr(cu_rows),
+                                       _addr(start_pos), _addr(page_table), _addr(kpool), _addr(vpool),
+                                       _addr(k_factors), _addr(v_factors), _stream(stream)),
+           "kpa_paged_read_factors")
+
+
+def kpa_paged_prefill_workspace_size(cfg, pages, batch, n_rows, max_len, window=0, sinks=0) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.kpa_paged_prefill_workspace_size(ctypes.byref(cfg), ctypes.byref(pages), batch, n_rows, max_len,
+                                                 window, sinks, ctypes.byref(n)),
+           "kpa_paged_prefill_workspace_size")
+    return n.value
+
+
+def kpa_paged_prefill(cfg, pages, batch, n_rows, q, cu_rows, start_pos, page_table, kpool, vpool, max_len, window,
+                      sinks, sm_scale, out, workspace=None, ws_bytes=None, stream=None):
+    """Attention of each sequence's chunk of new rows over its pages (window 0: every slot up
+    to the row's own)."""
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.kpa_paged_prefill(ctypes.byref(cfg), ctypes.byref(pages), batch, n_rows, _addr(q), _addr(cu_rows),
+                                  _addr(start_pos), _addr(page_table), _addr(kpool), _addr(vpool), max_len, window,
+                                  sinks, sm_scale, _addr(out), _addr(workspace), ws_bytes, _stream(stream)),
+           "kpa_paged_prefill")
+
+
+def kpa_paged_decode_workspace_size(cfg, pages, batch, max_len, window=0, sinks=0) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.kpa_paged_decode_workspace_size(ctypes.byref(cfg), ctypes.byref(pages), batch, max_len, window, sinks,
+                                                ctypes.byref(n)), "kpa_paged_decode_workspace_size")
+    return n.value
+
+
+def kpa_paged_decode(cfg, pages, batch, q, seq_len, page_table, kpool, vpool, max_len, window, sinks, sm_scale, out,
+                     workspace=None, ws_bytes=None, stream=None):
+    """Attention of one token per sequence, at position seq_len[b] - 1, over its pages."""
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.kpa_paged_decode(ctypes.byref(cfg), ctypes.byref(pages), batch, _addr(q), _addr(seq_len),
+                                 _addr(page_table), _addr(kpool), _addr(vpool), max_len, window, sinks, sm_scale,
+                                 _addr(out), _addr(workspace), ws_bytes, _stream(stream)), "kpa_paged_decode")
+
+
 def kpa_test_exp2_poly(x, y, stream=None):
     """y = 2^x (float32 device tensors of the same size) through the prefill's
     polynomial exponential (testing)."""
@@ -316,4 +404,4 @@ def kpa_read_device_error(stream=None) -> int:
 
 
 __all__ = [n for n in list(globals()) if n.startswith("kpa_") or n.startswith("KPA_")] + [
-    "KpaError", "make_config", "LIB_PATH"]
+    "KpaError", "make_config", "make_pages", "LIB_PATH"]

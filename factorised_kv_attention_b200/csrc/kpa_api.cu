@@ -251,6 +251,12 @@ kpa_status plan_decode(const Dims &d, kpa_dtype dt, int batch, int max_len, int 
 
 void record_cuda_error(cudaError_t e) { t_last_cuda = (int)e; }
 
+kpa_status config_check(const kpa_config *cfg) { return check_cfg(cfg, false, false); }
+Dims config_dims(const kpa_config *cfg) { return dims_of(cfg); }
+RopeTable config_rope(const kpa_config *cfg) { return rope_table(cfg); }
+kpa_status device_info(int **err, int *sms) { return device_state(err, sms); }
+unsigned long long device_wait_limit_ns() { return current_hooks().wait_limit_ns; }
+
 kpa_status decode_dense_plan(const kpa_config *cfg, int batch, int max_len, size_t *total, size_t *offset,
                              size_t *bytes) {
     kpa_status s = check_cfg(cfg, false, false);

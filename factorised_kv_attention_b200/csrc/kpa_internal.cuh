@@ -103,6 +103,15 @@ inline cudaError_t ensure_dynamic_smem(size_t bytes) {
 // Remember a CUDA error for kpa_last_cuda_error (calling thread).
 void record_cuda_error(cudaError_t e);
 
+// Shared by the entry points of every file: the shape checks of a config, its derived
+// sizes and RoPE frequencies, the current device's error word and SM count, and the
+// calling thread's bound on device waits.
+kpa_status config_check(const kpa_config *cfg);
+Dims config_dims(const kpa_config *cfg);
+RopeTable config_rope(const kpa_config *cfg);
+kpa_status device_info(int **err, int *sms);
+unsigned long long device_wait_limit_ns();
+
 // ---- host-side launchers (one per kernel file) ------------------------------
 // pos_offset (nullable, device [batch]): the keys of slot s are rotated at position
 // s + pos_offset[b] instead of s

@@ -1,0 +1,183 @@
+// kpa_paged.cuh -- the paged factor cache as the kernels see it: where a slot lies, which
+// slots a row sees, and which rows belong to which sequence.
+#pragma once
+
+#include "kpa_internal.cuh"
+
+namespace kpa {
+namespace paged {
+
+constexpr int kSlots16 = 16;         // slots per addressed group (two 8-slot groups in a bf16 page)
+
+// One pool and its page table.  Both formats are addressed by groups of 16 slots: a group
+// of a plane is one contiguous run of kg (vg) bytes, E * 32 in bf16, (E + 2) * 16 in e4m3.
+struct Pool {
+    const unsigned char *k, *v;
+    const int32_t *table;
+    int table_stride;
+    int n_pages;
+    int pg;                          // groups per page
+    unsigned long long magic;        // ceil(2^36 / pg): group / pg = group * magic >> 36 for group < 2^27, pg <= 2^8
+    int kg, vg;                      // bytes per group of a plane
+    int e4m3;
+};
+
+// Page table entry index and group inside the page of 16-slot group g of a sequence.
+__device__ __forceinline__ void split_group(const Pool &p, int g, int &entry, int &in) {
+    entry = (int)(((unsigned long long)(unsigned)g * p.magic) >> 36);
+    in = g - entry * p.pg;
+}
+
+// Which slots a row at position pos sees: [0, sinks) and [pos - window + 1, pos].  lo is the
+// start of the window for the first (smallest) position of a set of rows.
+struct Mask {
+    int window, sinks;
+};
+__host__ __device__ __forceinline__ int window_start(const Mask &m, int pos) {
+    return m.window > 0 && pos >= m.window ? pos - m.window + 1 : 0;
+}
+__device__ __forceinline__ bool sees(const Mask &m, int pos, int s) {
+    return s <= pos && (m.window == 0 || pos - s < m.window || s < m.sinks);
+}
+
+// The tiles (T slots each, aligned to T) that rows at positions lo .. hi see between them:
+// tiles [0, head) hold the sinks and [first, last] the windows; tile v of n is v or v + gap.
+struct Tiles {
+    int head, gap, n;
+    __device__ __forceinline__ int slot_tile(int v) const { return v < head ? v : v + gap; }
+};
+__device__ __forceinline__ Tiles visible_tiles(const Mask &m, int lo, int hi, int T) {
+    Tiles t;
+    const int first = window_start(m, lo) / T, last = hi / T;
+    const int sink_tiles = m.window > 0 ? (min(m.sinks, hi + 1) + T - 1) / T : 0;
+    t.head = min(sink_tiles, first);
+    t.gap = first - t.head;
+    t.n = t.head + (last - first + 1);
+    return t;
+}
+
+// Rows of one sequence: checked against [0, n_rows]; false (no rows) where they are not.
+__device__ __forceinline__ bool rows_of(const int32_t *cu, int b, int n_rows, int &r0, int &r1) {
+    r0 = cu[b];
+    r1 = cu[b + 1];
+    return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
+}
+
+// Finds the sequence that unit `idx` falls to when sequence b has count(b, bad) units, laid
+// one sequence after the other.  Every thread of the block calls it; returns the sequence
+// (or -1 past the last unit) and the unit's index inside it.  THREADS threads, a scan of
+// THREADS sequences per step, to the end of the batch for the block that reports bad ones.
+struct Found {
+    int b, i;
+};
+template <int THREADS, class Count>
+__device__ __forceinline__ Found find_unit(int idx, int batch, bool to_end, Count count) {
+    __shared__ int warp_sum[THREADS / 32];
+    __shared__ int hit_b, hit_i;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) hit_b = -1;
+    int before = 0;
+    for (int base = 0; base < batch; base += THREADS) {
+        const int b = base + tid;
+        const int c = b < batch ? count(b) : 0;
+        int inc = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        int pre = before, total = before;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            const int s = warp_sum[w];
+            if (w < warp) pre += s;
+            total += s;
+        }
+        const int lo = pre + inc - c;
+        if (idx >= lo && idx < lo + c) {
+            hit_b = b;
+            hit_i = idx - lo;
+        }
+        __syncthreads();
+        before = total;
+        if (idx < before && !to_end) break;
+    }
+    Found f;
+    f.b = hit_b;
+    f.i = hit_i;
+    __syncthreads();
+    return f;
+}
+
+// ---- e4m3
+// two e4m3 codes (low byte first) as fp16x2
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+// (lo, hi) floats as two e4m3 codes, nearest even, saturating at 448; NaN stays NaN
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f32 c, %1, %2;\n\tcvt.u32.u16 %0, c;\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 h2_to_f2(uint32_t w) {
+    float2 f;
+    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(w));
+    return f;
+}
+// 2^(byte - 127) for byte in [1, 254]
+__device__ __forceinline__ float exp_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
+// Four slots' exponent bytes of the A row and of the B row (each in [63, 190] for a slot that
+// was written) to the bytes of their products' exponents: 2^(a - 127) 2^(b - 127) =
+// 2^((a + b - 126) - 128), a + b - 126 in [0, 254].  Each byte's sum is taken modulo 256
+// without a carry into its neighbour: an unwritten slot beside may hold anything.
+__device__ __forceinline__ uint32_t exp_sum4(uint32_t a4, uint32_t b4) {
+    const uint32_t t = ((a4 & 0x7f7f7f7fu) + (b4 & 0x7f7f7f7fu)) ^ ((a4 ^ b4) & 0x80808080u);
+    return ((t & 0x7f7f7f7fu) + 0x02020202u) ^ (~t & 0x80808080u);          // + 130 = - 126
+}
+// 2^(byte - 128), byte in [0, 254]: half of 2^(byte - 127) (byte 0: 2^-128 as a denormal)
+__device__ __forceinline__ float exp_sum(uint32_t byte) { return 0.5f * __uint_as_float(byte << 23); }
+
+}  // namespace paged
+
+// ---- host-side launchers
+struct PagedShape {
+    Dims d;
+    paged::Pool pool;
+};
+
+cudaError_t launch_paged_append(const PagedShape &s, int batch, int n_rows, const void *kf, const void *vf,
+                                const int32_t *cu, const int32_t *start, void *kpool, void *vpool,
+                                const RopeTable &rope, int *err, cudaStream_t st);
+cudaError_t launch_paged_read(const PagedShape &s, int batch, int n_rows, const int32_t *cu, const int32_t *start,
+                              void *kf, void *vf, int *err, cudaStream_t st);
+
+// Attention of rows (cu, start) or, with cu null, of one row per sequence at position
+// seq_len[b] - 1.
+struct PagedAttnArgs {
+    const __nv_bfloat16 *q;
+    const int32_t *cu, *start, *seq_len;
+    int batch, n_rows, max_len;
+    paged::Mask mask;
+    float qscale;                 // sm_scale / R_K * log2(e)
+    float out_scale;              // 1 / R_V
+    __nv_bfloat16 *out;
+    float *part_o, *part_ml;      // n_split > 1: [n_rows][h][n_split][d_h] and [n_rows][h][n_split][2]
+    int n_split;
+    int *err;
+};
+
+bool paged_mma_supported(const Dims &d, bool e4m3);
+int paged_mma_rows();                                        // rows of a tile
+cudaError_t launch_paged_mma(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
+
+}  // namespace kpa

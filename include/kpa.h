@@ -330,6 +330,111 @@ kpa_status kpa_append(const kpa_config *cfg, int32_t batch, int32_t n_tok, const
                       void *kcache, void *vcache, void *q_out, void *workspace,
                       size_t ws_bytes, kpa_stream stream);
 
+/* ---------------------------------------------------------------- paged factor cache
+ * A cache whose slots lie in pages of a pool shared by all sequences.  The pool is two
+ * planes (keys, values) of n_pages pages; page_table[b * table_stride + i] (int32) names
+ * the page of sequence b's slots i * page_size .. i * page_size + page_size - 1.  Slot s
+ * holds the token at position s; keys are stored with B^K rotated.
+ *
+ * KPA_PAGE_BF16: a page of a plane has the layout of the contiguous cache above with
+ *   capacity = page_size (groups of 8 slots, element-major, token-minor).
+ * KPA_PAGE_E4M3: groups of 16 slots; a group is E + 2 rows of 16 bytes, slot t of the
+ *   group at byte 2 (t mod 8) + t / 8 of each row.  Rows 0 .. E-1 hold the record's
+ *   elements as e4m3 codes, row E the exponent byte of each slot's A factors and row
+ *   E + 1 that of its B factors (E8M0: scale 2^(byte - 127)); an element is its code
+ *   times the scale of its part.  The scale of a part is the smallest 2^e, e in
+ *   [-64, 63], with 448 * 2^e >= every finite |x| of the part (e = -64 when they are all
+ *   zero); x / 2^e is rounded once to e4m3 (nearest even, saturating at 448), and a
+ *   non-finite x becomes NaN.  Scaling by powers of two is exact, so a value read back
+ *   as bf16 is exactly the value attention uses.
+ *
+ * Every call below takes order-2 caches with separate B factors (shared_b == 0) and
+ * cfg->dtype == KPA_BF16 (the type of factors, queries and outputs); other configs return
+ * KPA_ERR_UNSUPPORTED.
+ *
+ * Rows.  The calls that take several tokens per sequence take them flattened: sequence
+ * b's rows are cu_rows[b] .. cu_rows[b+1] - 1 of n_rows (cu_rows: device [batch + 1]
+ * int32, ascending), row cu_rows[b] + t at position start_pos[b] + t.  A sequence may have
+ * no rows.  Rows of no sequence (before cu_rows[0], or at and behind cu_rows[batch]) are
+ * neither read nor written.  A sequence whose cu_rows descend or leave [0, n_rows] sets
+ * KPA_ERR_DEVICE_CHECK and is skipped.
+ *
+ * Page table entries are looked at only for slots that the call writes or that some of its
+ * rows see; the others may hold anything.  An entry outside [0, n_pages) sets
+ * KPA_ERR_DEVICE_CHECK: nothing is written to it, a read returns zeros for it, and the
+ * attention of the rows that see it is unspecified. */
+typedef enum { KPA_PAGE_BF16 = 0, KPA_PAGE_E4M3 = 1 } kpa_page_format;
+
+typedef struct {
+    int32_t page_size;        /* slots per page: a multiple of 16, at most 4096        */
+    int32_t n_pages;          /* pages of each plane of the pool                       */
+    int32_t table_stride;     /* entries of a page table row; page_size * table_stride
+                               * slots at most a sequence (below 2^31)                 */
+    kpa_page_format format;
+} kpa_pages;
+
+/* Bytes of one page of the key plane and of the value plane (a plane is n_pages times
+ * that).  Either output may be NULL.  Host only. */
+kpa_status kpa_paged_page_bytes(const kpa_config *cfg, const kpa_pages *pages, size_t *k_bytes, size_t *v_bytes);
+
+/* Write new tokens' factor records into their pages, B^K rotated at the token's position
+ * and, for an e4m3 pool, quantised as above.
+ *   k_factors [n_rows][E_K], v_factors [n_rows][E_V]  unrotated records, bf16
+ * A token whose slot is negative or outside the table's range is not written and sets
+ * KPA_ERR_DEVICE_CHECK.  Two rows of one call must not name one slot of the pool. */
+kpa_status kpa_paged_append_factors(const kpa_config *cfg, const kpa_pages *pages, int32_t batch, int32_t n_rows,
+                                    const void *k_factors, const void *v_factors, const int32_t *cu_rows,
+                                    const int32_t *start_pos, const int32_t *page_table, void *kpool, void *vpool,
+                                    kpa_stream stream);
+
+/* Read records back as bf16: row cu_rows[b] + t receives slot start_pos[b] + t as cached
+ * (keys with B^K rotated).  A slot that is negative or outside the table's range gives a
+ * row of zeros and sets KPA_ERR_DEVICE_CHECK. */
+kpa_status kpa_paged_read_factors(const kpa_config *cfg, const kpa_pages *pages, int32_t batch, int32_t n_rows,
+                                  const int32_t *cu_rows, const int32_t *start_pos, const int32_t *page_table,
+                                  const void *kpool, const void *vpool, void *k_factors, void *v_factors,
+                                  kpa_stream stream);
+
+/* Attention of a chunk of new tokens per sequence over a paged cache.  The row at position
+ * p sees slot s when 0 <= s <= p and (window == 0, or p - s < window, or s < sinks): a
+ * sliding window of `window` tokens, its own included, beside the first `sinks` tokens.
+ * The rows' own tokens must already be in the cache (kpa_paged_append_factors).
+ *   q    [n_rows][h][d_h]  bf16, already rotated
+ *   out  [n_rows][h][d_h]  bf16
+ *   max_len  every position is below max_len (at most page_size * table_stride); a row at
+ *        or above it, or below 0, gets zeros and sets KPA_ERR_DEVICE_CHECK
+ *   window >= 0, sinks >= 0
+ *   workspace at least kpa_paged_prefill_workspace_size bytes, 256-byte aligned; it needs
+ *        no initialisation and holds nothing between calls
+ * K and V are rebuilt from the factors on chip and rounded once to fp16; products
+ * accumulate in fp32, and the softmax is fp32.  A cached value that is not finite, or a
+ * rebuilt one outside fp16's range, makes the rows that see it, and possibly other rows of
+ * the same sequence and call, non-finite and sets KPA_ERR_DEVICE_CHECK; slots that none of
+ * the sequence's rows sees, whatever they hold, change nothing.
+ * Takes every split with d_h <= 128 that kpa_prefill takes.  Results are deterministic. */
+kpa_status kpa_paged_prefill_workspace_size(const kpa_config *cfg, const kpa_pages *pages, int32_t batch,
+                                            int32_t n_rows, int32_t max_len, int32_t window, int32_t sinks,
+                                            size_t *bytes);
+kpa_status kpa_paged_prefill(const kpa_config *cfg, const kpa_pages *pages, int32_t batch, int32_t n_rows,
+                             const void *q, const int32_t *cu_rows, const int32_t *start_pos,
+                             const int32_t *page_table, const void *kpool, const void *vpool, int32_t max_len,
+                             int32_t window, int32_t sinks, float sm_scale, void *out, void *workspace,
+                             size_t ws_bytes, kpa_stream stream);
+
+/* The same attention for one token per sequence: the query is at position seq_len[b] - 1,
+ * the newest slot.
+ *   q    [batch][h][d_h]  bf16, already rotated
+ *   seq_len [batch] int32  0 <= seq_len[b] <= max_len; a longer length is clamped to
+ *        max_len, a negative one to 0, and sets KPA_ERR_DEVICE_CHECK; 0 gives zeros
+ *   out  [batch][h][d_h]  bf16
+ * Other rules as kpa_paged_prefill. */
+kpa_status kpa_paged_decode_workspace_size(const kpa_config *cfg, const kpa_pages *pages, int32_t batch,
+                                           int32_t max_len, int32_t window, int32_t sinks, size_t *bytes);
+kpa_status kpa_paged_decode(const kpa_config *cfg, const kpa_pages *pages, int32_t batch, const void *q,
+                            const int32_t *seq_len, const int32_t *page_table, const void *kpool, const void *vpool,
+                            int32_t max_len, int32_t window, int32_t sinks, float sm_scale, void *out,
+                            void *workspace, size_t ws_bytes, kpa_stream stream);
+
 /* Upper bound, in bytes, of the scratch that kpa_decode_noalloc can use. */
 #define KPA_DECODE_NOALLOC_MAX_BYTES (16u << 20)
 
