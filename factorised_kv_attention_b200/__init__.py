@@ -102,6 +102,8 @@ _SIGS = {
     "kpa_paged_prefill": ([_cfgp, _pgp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp,
                            _sz, _vp], ctypes.c_int),
     "kpa_paged_decode_workspace_size": ([_cfgp, _pgp, _i32, _i32, _i32, _i32, _szp], ctypes.c_int),
+    "kpa_paged_decode_kernel_kind": ([_cfgp, _pgp, _i32p], ctypes.c_int),
+    "kpa_paged_prefill_kernel_kind": ([_cfgp, _pgp, _i32p], ctypes.c_int),
     "kpa_paged_decode": ([_cfgp, _pgp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp],
                          ctypes.c_int),
 }
@@ -387,6 +389,25 @@ def kpa_paged_decode(cfg, pages, batch, q, seq_len, page_table, kpool, vpool, ma
     _check(_lib.kpa_paged_decode(ctypes.byref(cfg), ctypes.byref(pages), batch, _addr(q), _addr(seq_len),
                                  _addr(page_table), _addr(kpool), _addr(vpool), max_len, window, sinks, sm_scale,
                                  _addr(out), _addr(workspace), ws_bytes, _stream(stream)), "kpa_paged_decode")
+
+
+PAGED_KERNEL_NAMES = {0: "chunks", 1: "factors", 2: "tcgen05"}
+
+
+def kpa_paged_decode_kernel_kind(cfg, pages):
+    """Name of the kernel kpa_paged_decode runs for this config and pool."""
+    k = ctypes.c_int32()
+    _check(_lib.kpa_paged_decode_kernel_kind(ctypes.byref(cfg), ctypes.byref(pages), ctypes.byref(k)),
+           "kpa_paged_decode_kernel_kind")
+    return PAGED_KERNEL_NAMES[k.value]
+
+
+def kpa_paged_prefill_kernel_kind(cfg, pages):
+    """Name of the kernel kpa_paged_prefill runs for this config and pool."""
+    k = ctypes.c_int32()
+    _check(_lib.kpa_paged_prefill_kernel_kind(ctypes.byref(cfg), ctypes.byref(pages), ctypes.byref(k)),
+           "kpa_paged_prefill_kernel_kind")
+    return PAGED_KERNEL_NAMES[k.value]
 
 
 def kpa_test_exp2_poly(x, y, stream=None):

@@ -180,4 +180,11 @@ int paged_mma_rows();                                        // rows of a tile
 cudaError_t launch_paged_mma(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 
+// The single-token kernel: its variant for these dims (-1: none, the chunk kernel takes
+// them), the 16-slot groups of its tiles and its CTAs per SM, and its launcher.
+int paged_decode_variant(const Dims &d);
+void paged_decode_shape(int variant, bool e4m3, int *tile_groups, int *ctas_per_sm);
+cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &a, int groups_per_split,
+                                unsigned long long wait_limit_ns, cudaStream_t st);
+
 }  // namespace kpa

@@ -42,24 +42,55 @@ kpa_status check_paged(const kpa_config *cfg, const kpa_pages *pg, PagedShape *s
 }
 
 struct AttnPlan {
+    int variant;                 // of the single-token kernel, or -1: the chunk kernel
+    int groups_per_split;        // (single-token kernel)
     int n_split;
     size_t ml_off, bytes;
 };
 
-// How the rows' key range is split: when there are fewer CTAs than two per SM, into as
-// many runs as make up for it, of at least four tiles (256 slots) each: shorter ones cost
-// more in partials than they gain.
-AttnPlan plan_attn(const Dims &d, int batch, int n_rows, bool chunks, int max_len, int window, int sinks, int sms) {
-    constexpr int kTile = 64, kMinTiles = 4;
+// How the rows' key range is split.
+//  - The chunk kernel: when there are fewer CTAs than two per SM, into as many runs as make
+//    up for it, of at least four tiles (256 slots) each: shorter ones cost more in partials
+//    than they gain.
+//  - The single-token kernel: one CTA per slot of the SMs for a single sequence; several
+//    sequences may have different lengths (the host does not see them), so up to four times
+//    as many shorter runs let the CTA scheduler even them out, as long as a run keeps eight
+//    tiles.
+AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int max_len, int window, int sinks,
+                   int sms) {
+    const Dims &d = ps.d;
+    const bool e4m3 = ps.pool.e4m3 != 0;
+    AttnPlan p = {};
+    p.variant = chunks ? -1 : paged_decode_variant(d);
     const int tr = paged_mma_rows();
-    const int64_t row_tiles = chunks ? std::max<int64_t>((n_rows + tr - 1) / tr, std::min(batch, n_rows)) : batch;
-    const int64_t ctas = std::max<int64_t>(1, row_tiles * d.h);
-    int64_t vis = ((int64_t)max_len + kTile - 1) / kTile;
-    if (window > 0)
-        vis = std::min(vis, ((int64_t)sinks + kTile - 1) / kTile + ((int64_t)window + (chunks ? tr : 1)) / kTile + 2);
-    int64_t s = std::min((2 * (int64_t)sms + ctas - 1) / ctas, vis / kMinTiles);
-    AttnPlan p;
-    p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(s, 4096));
+    auto visible = [&](int64_t T, int64_t rows) {          // units of T slots that a set of rows sees at most
+        const int64_t all = ((int64_t)max_len + T - 1) / T;
+        return window > 0 ? std::min(all, ((int64_t)sinks + T - 1) / T + ((int64_t)window + rows) / T + 2) : all;
+    };
+    if (p.variant >= 0) {
+        int tg = 1, per_sm = 1;
+        paged_decode_shape(p.variant, e4m3, &tg, &per_sm);
+        const int64_t groups = std::max<int64_t>(1, visible(16, 1)), tiles = (groups + tg - 1) / tg;
+        const int64_t per_seq = std::max<int64_t>(1, (int64_t)sms * per_sm / batch);
+        int64_t per = (tiles + per_seq - 1) / per_seq;
+        if (batch > 1)
+            for (int k = 4; k > 1; --k) {
+                const int64_t t = (tiles + per_seq * k - 1) / (per_seq * k);
+                if (t >= 8) {
+                    per = t;
+                    break;
+                }
+            }
+        p.groups_per_split = (int)(per * tg);
+        p.n_split = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
+    } else {
+        constexpr int kTile = 64, kMinTiles = 4;
+        const int64_t row_tiles = chunks ? std::max<int64_t>((n_rows + tr - 1) / tr, std::min(batch, n_rows)) : batch;
+        const int64_t ctas = std::max<int64_t>(1, row_tiles * d.h);
+        const int64_t s =
+            std::min((2 * (int64_t)sms + ctas - 1) / ctas, visible(kTile, chunks ? tr : 1) / kMinTiles);
+        p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(s, 4096));
+    }
     const size_t rh = (size_t)n_rows * d.h * p.n_split;
     p.ml_off = (rh * d.dh * sizeof(float) + 255) & ~(size_t)255;
     p.bytes = p.n_split > 1 ? p.ml_off + ((rh * 2 * sizeof(float) + 255) & ~(size_t)255) : 0;
@@ -74,7 +105,7 @@ kpa_status check_attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch,
     if ((int64_t)max_len > (int64_t)pg->page_size * pg->table_stride) return KPA_ERR_INVALID_ARG;
     if (st != KPA_OK) return st;
     if (!paged_mma_supported(s->d, s->pool.e4m3 != 0)) return KPA_ERR_UNSUPPORTED;
-    if (n_rows > INT32_MAX / 2 || batch > INT32_MAX / 256) return KPA_ERR_UNSUPPORTED;
+    if (n_rows > INT32_MAX / 2 || batch > 65535) return KPA_ERR_UNSUPPORTED;
     return KPA_OK;
 }
 
@@ -89,7 +120,7 @@ kpa_status workspace_size(const kpa_config *cfg, const kpa_pages *pg, int32_t ba
     int sms = 0;
     st = device_info(nullptr, &sms);
     if (st != KPA_OK) return st;
-    *bytes = plan_attn(s.d, batch, n_rows, chunks, max_len, window, sinks, sms).bytes;
+    *bytes = plan_attn(s, batch, n_rows, chunks, max_len, window, sinks, sms).bytes;
     return KPA_OK;
 }
 
@@ -111,7 +142,7 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
     int *err = nullptr, sms = 0;
     st = device_info(&err, &sms);
     if (st != KPA_OK) return st;
-    const AttnPlan p = plan_attn(s.d, batch, n_rows, chunks, max_len, window, sinks, sms);
+    const AttnPlan p = plan_attn(s, batch, n_rows, chunks, max_len, window, sinks, sms);
     if (p.bytes > 0) {
         if (!workspace || ws_bytes < p.bytes) return KPA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return KPA_ERR_INVALID_ARG;
@@ -138,7 +169,9 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.ml_off);
     }
     a.err = err;
-    const cudaError_t e = launch_paged_mma(s, a, (cudaStream_t)stream);
+    const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split,
+                                                               device_wait_limit_ns(), (cudaStream_t)stream)
+                                         : launch_paged_mma(s, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KPA_OK : fail(e);
 }
 
@@ -221,6 +254,24 @@ kpa_status kpa_paged_prefill(const kpa_config *cfg, const kpa_pages *pages, int3
                              size_t ws_bytes, kpa_stream stream) {
     return attn(cfg, pages, batch, n_rows, true, q, cu_rows, start_pos, nullptr, page_table, kpool, vpool, max_len,
                 window, sinks, sm_scale, out, workspace, ws_bytes, stream);
+}
+
+static kpa_status kernel_kind(const kpa_config *cfg, const kpa_pages *pages, bool chunks, int32_t *kind) {
+    PagedShape s;
+    const kpa_status st = check_paged(cfg, pages, &s);
+    if (st != KPA_OK) return st;
+    if (!kind) return KPA_ERR_INVALID_ARG;
+    if (!paged_mma_supported(s.d, s.pool.e4m3 != 0)) return KPA_ERR_UNSUPPORTED;
+    *kind = !chunks && paged_decode_variant(s.d) >= 0 ? KPA_PAGED_KERNEL_FACTORS : KPA_PAGED_KERNEL_CHUNKS;
+    return KPA_OK;
+}
+
+kpa_status kpa_paged_decode_kernel_kind(const kpa_config *cfg, const kpa_pages *pages, int32_t *kind) {
+    return kernel_kind(cfg, pages, false, kind);
+}
+
+kpa_status kpa_paged_prefill_kernel_kind(const kpa_config *cfg, const kpa_pages *pages, int32_t *kind) {
+    return kernel_kind(cfg, pages, true, kind);
 }
 
 kpa_status kpa_paged_decode_workspace_size(const kpa_config *cfg, const kpa_pages *pages, int32_t batch,

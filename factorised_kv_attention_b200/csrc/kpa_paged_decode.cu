@@ -1,0 +1,793 @@
+// kpa_paged_decode.cu -- single-token attention over a paged factor cache on the tensor
+// cores, for the head splits of KPA_PAGED_DECODE_VARIANTS (every other one runs on the
+// chunk kernel).
+//
+// Proposition 2.2 of "Kronecker Product Attention" with a dense query, per 16-slot group:
+//   T_r[(i1,j1), s] = sum_j2 q[(i1,i2),(j1,j2)] B^K_r(s)[i2,j2]         (mma.sync m16n8k16)
+//   score[(i1,i2), s] = sum_r sum_j1 A^K_r(s)[i1,j1] T_r[(i1,j1), s]
+//   O_i2[(i1,j1), j2] += sum_{s,r} (p[(i1,i2), s] A^V_r(s)[i1,j1]) B^V_r(s)[i2,j2]
+// One warp takes 16 slots of one i2.  The query is exact in the operand type (bf16 over a
+// bf16 pool, fp16 over an e4m3 one, whose codes are exact in fp16), so the score products
+// run once; p A^V is rounded once to fp16 (2^-11 relative).  Sums, scores and the softmax
+// are fp32.  With d1 = 8 the rows of an m-tile pair up two j1 of one head per lane, so the
+// sum over j1 is one add and two shuffles; with d1 = 1 (TPA) rows are heads.
+//
+// An e4m3 token's two key scales multiply its score (one number per token: the scales of a
+// Kronecker product's factors multiply), its two value scales its B^V in fp16, times 2^8 that
+// the output takes back, so codes near 448 and usual magnitudes both sit well inside fp16.
+//
+// Data movement: 16-slot groups are contiguous in the pool, so each is one cp.async.bulk per
+// plane through the page table into a ring of STAGES tiles; the last warp to release a stage
+// issues its next tile.  The table entries of that tile are fetched while the current one is
+// computed.  Only groups with a visible slot are copied; the slots of such a group that the
+// query does not see are masked in the scores and zeroed in the value operands, so their
+// bytes may hold anything.  Waits are bounded.
+#include "kpa_f32x2.cuh"
+#include "kpa_paged.cuh"
+#include "kpa_sm100.cuh"
+
+#include <type_traits>
+
+namespace kpa {
+namespace {
+
+using namespace paged;
+using f32x2::ffma2;
+using f32x2::fmul2;
+using f32x2::unpack_bf16x2;
+using sm100::bulk_g2s;
+using sm100::mbar_expect_tx;
+using sm100::mbar_init;
+using sm100::mbar_wait;
+using sm100::smem_u32;
+
+struct DecodeArgsP {
+    PagedAttnArgs p;
+    Pool pool;
+    int gps;                      // 16-slot groups per split
+    unsigned long long limit_ns;
+};
+
+// MA = h1*d1 rows of the products of one i2, SLICES token slices per CTA, HS warps that share
+// a slice's 16-row tiles, CHUNKS groups per warp and tile, STAGES tiles in the ring.
+template <int MA_, int D1_, int D2_, int RK_, int RV_, int H2_, int SLICES_, int HS_, int CHUNKS_, int STAGES_, bool Q8_>
+struct Cfg {
+    static constexpr int MA = MA_, D1 = D1_, D2 = D2_, RK = RK_, RV = RV_, H2 = H2_;
+    static constexpr int SLICES = SLICES_, HS = HS_, CHUNKS = CHUNKS_, STAGES = STAGES_;
+    static constexpr bool Q8 = Q8_, KPA = D1 == 8;
+    static constexpr int H1 = MA / D1, H = H1 * H2, DH = D1 * D2;
+    static constexpr int EK = RK * (MA + H2 * D2), EV = RV * (MA + H2 * D2);
+    static constexpr int KG = Q8 ? (EK + 2) * 16 : EK * 32, VG = Q8 ? (EV + 2) * 16 : EV * 32;
+    static constexpr int WARPS = H2 * SLICES * HS, THREADS = WARPS * 32;
+    static constexpr int TG = SLICES * CHUNKS;                     // groups per tile
+    static constexpr int STAGE_BYTES = TG * (KG + VG);
+    static constexpr int MT = MA / 16 / HS;                        // 16-row tiles of a warp
+    static constexpr int HR = KPA ? 1 : 2;                         // heads of a lane per tile
+    static constexpr int MO_LD = DH + 8;                           // padded rows of the slice merge
+    static constexpr size_t OFF_BARS = (size_t)STAGES * STAGE_BYTES;
+    static constexpr size_t OFF_TAB = OFF_BARS + 8 * STAGES;                         // group indices of the next tiles
+    static constexpr size_t OFF_FLAGS = OFF_TAB + 8 * STAGES * TG;                   // [0] abort, [1 + s] releases
+    static constexpr size_t SMEM = OFF_FLAGS + 4 * (1 + STAGES);
+    static_assert(MA % (16 * HS) == 0 && (KPA || (D1 == 1 && H2 == 1)) && (!KPA || HS == 1), "shape");
+    static_assert(D2 % 16 == 0 || (KPA && D2 == 8), "d2");
+    static_assert(WARPS <= 16 && STAGES * TG <= 32, "one warp issues the first ring");
+    static_assert((size_t)SLICES * H * (MO_LD + 2) * 4 <= (size_t)STAGES * STAGE_BYTES, "slice merge fits in the ring");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t *r, std::integral_constant<int, 4>, std::false_type) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t *r, std::integral_constant<int, 4>, std::true_type) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t *r, std::integral_constant<int, 2>, std::false_type) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t *r, std::integral_constant<int, 2>, std::true_type) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+// N 8 x 8 matrices, matrix j's row `lane & 7` at row_of(j) * 16 bytes behind base
+template <int N, bool TRANS, class RowOf>
+__device__ __forceinline__ void ldsm_list(uint32_t base, int lane, uint32_t (&w)[N], RowOf row_of) {
+    static_assert(N % 4 == 0 || N == 2, "matrices in fours, or two");
+    if constexpr (N == 2) {
+        ldsm(base + row_of((lane >> 3) & 1) * 16, w, std::integral_constant<int, 2>{}, std::bool_constant<TRANS>{});
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+            ldsm(base + row_of(j + (lane >> 3)) * 16, w + j, std::integral_constant<int, 4>{}, std::bool_constant<TRANS>{});
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
+    else
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_h2(uint32_t v) {
+    const float2 x = unpack_bf16x2(v);
+    return pack_h2(x.x, x.y);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t mask_pair(uint32_t v, bool k0, bool k1) {
+    return (k0 ? (v & 0xffffu) : 0u) | (k1 ? (v & 0xffff0000u) : 0u);
+}
+// Four e4m3 bytes of a group row or column pair, in the order slot, slot + 8 of one value,
+// then of the next: the two values of the lower slots and of the upper slots, as fp16x2.
+__device__ __forceinline__ void e4m3_split(uint32_t w, uint32_t &lower, uint32_t &upper) {
+    const uint32_t v = __byte_perm(w, 0, 0x3120);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lower), "=r"(upper)
+        : "r"(v));
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const DecodeArgsP a) {
+    constexpr int MA = C::MA, D1 = C::D1, D2 = C::D2, RK = C::RK, RV = C::RV, H2 = C::H2, H = C::H, DH = C::DH;
+    constexpr int MT = C::MT, HR = C::HR, NT = D2 / 8, KS = D2 == 8 ? 1 : D2 / 16;
+    constexpr int TG = C::TG, STAGES = C::STAGES, WARPS = C::WARPS, CHUNKS = C::CHUNKS, SLICES = C::SLICES, HS = C::HS;
+    constexpr int KG = C::KG, VG = C::VG, A_K = RK * MA, A_V = RV * MA;
+    constexpr bool Q8 = C::Q8, KPA = C::KPA;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t full0 = smem_u32(smem + C::OFF_BARS);
+    size_t *tab = reinterpret_cast<size_t *>(smem + C::OFF_TAB);
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.y, split = blockIdx.x;
+    const int g = lane >> 2, c = lane & 3;
+    const int i2 = warp % H2, hs = (warp / H2) % HS, slice = warp / (H2 * HS);
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int i = 0; i < 1 + STAGES; ++i) flags[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- this CTA's groups: virtual groups v0 .. v1 - 1 of the sequence's visible ones
+    const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
+    int len = a.p.seq_len[b];
+    // without a window the first ring's table entries do not depend on the length: fetch them
+    // beside it (inside the row for every slot below max_len)
+    const int v0 = split * a.gps;
+    int first_entry = -1, first_page = 0, first_in = 0;
+    if (warp == 0 && lane < STAGES * TG && a.p.mask.window == 0 && (long long)(v0 + lane) * 16 < a.p.max_len) {
+        split_group(a.pool, v0 + lane, first_entry, first_in);
+        first_page = __ldg(trow + first_entry);
+    }
+    // query fragments (A operand): row g (g + 8) of tile mt is (i1, j1) = (2 mt + (g >> 2), 2 (g & 3)) and
+    // (i1, j1 + 1) with d1 = 8, head 16 mt + g (+ 8) with d1 = 1
+    uint32_t qa[MT][KS][4];
+    {
+        const uint32_t *qb = reinterpret_cast<const uint32_t *>(a.p.q + (size_t)b * H * DH);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v) {
+                    const int j2 = ks * 16 + 2 * c + ((v & 2) ? 8 : 0);
+                    int f;
+                    if constexpr (KPA)
+                        f = ((2 * mt + (g >> 2)) * H2 + i2) * DH + (2 * (g & 3) + (v & 1)) * D2 + j2;
+                    else
+                        f = ((hs * MT + mt) * 16 + g + 8 * (v & 1)) * DH + j2;
+                    const uint32_t w = __ldg(qb + f / 2);
+                    qa[mt][ks][v] = Q8 ? bf16x2_to_h2(w) : w;
+                }
+    }
+    if (len < 0 || len > a.p.max_len) {
+        if (split == 0 && tid == 0) raise_error(a.p.err, kErrDeviceCheck);
+        len = len < 0 ? 0 : a.p.max_len;
+    }
+    const int pos = len - 1;
+    Tiles tl = {0, 0, 0};
+    if (len > 0) tl = visible_tiles(a.p.mask, pos, pos, 16);
+    const int wstart = len > 0 ? window_start(a.p.mask, pos) : 0;
+    const int v1 = min(tl.n, v0 + a.gps);
+    if (v0 >= v1) {                                        // nothing here: zeros, or an empty partial
+        if (a.p.n_split == 1) {
+            for (int i = tid; i < H * DH; i += C::THREADS)
+                a.p.out[(size_t)b * H * DH + i] = __float2bfloat16_rn(0.f);
+        } else {
+            for (int i = tid; i < H; i += C::THREADS)
+                *reinterpret_cast<float2 *>(a.p.part_ml + ((size_t)(b * H + i) * a.p.n_split + split) * 2) =
+                    make_float2(-INFINITY, 0.f);
+        }
+        return;
+    }
+    const int n_tiles = (v1 - v0 + TG - 1) / TG;
+    __syncthreads();                                       // barriers initialised
+
+    auto group_index = [&](int page, int in) -> size_t {
+        if (page < 0 || page >= a.pool.n_pages) {
+            raise_error(a.p.err, kErrDeviceCheck);
+            page = 0;
+        }
+        return (size_t)page * a.pool.pg + in;
+    };
+    auto copy_group = [&](int stage, int i, size_t group) {
+        const uint32_t dst = smem_u32(smem) + stage * C::STAGE_BYTES + i * (KG + VG);
+        bulk_g2s(dst, a.pool.k + group * KG, KG, full0 + 8 * stage);
+        bulk_g2s(dst + KG, a.pool.v + group * VG, VG, full0 + 8 * stage);
+    };
+    auto groups_in = [&](int t) { return min(TG, v1 - v0 - t * TG); };
+    if (warp == 0) {                                       // the first ring: one lane per group
+        if (lane < STAGES && lane < n_tiles) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
+        __syncwarp();
+        if (lane < STAGES * TG && v0 + lane < v1) {
+            if (first_entry < 0) {
+                split_group(a.pool, tl.slot_tile(v0 + lane), first_entry, first_in);
+                first_page = __ldg(trow + first_entry);
+            }
+            copy_group(lane / TG, lane % TG, group_index(first_page, first_in));
+        }
+    }
+
+    float o[MT][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+    float m_run[MT][HR], l_run[MT][HR];                    // running max and this lane's share of the sum
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hr = 0; hr < HR; ++hr) {
+            m_run[mt][hr] = -INFINITY;
+            l_run[mt][hr] = 0.f;
+        }
+    bool aborted = false;
+
+    // rows (16 bytes each) of matrix j's fragments inside a group
+    const int mrow = lane & 7;
+    auto a_row = [&](int j) {                              // j = (r, mt, half)
+        const int r = j / (2 * MT), mt = (j / 2) % MT, hf = j & 1;
+        if constexpr (KPA) return r * MA + (2 * mt + (mrow >> 2)) * D1 + 2 * (mrow & 3) + hf;
+        return r * MA + (hs * MT + mt) * 16 + hf * 8 + mrow;
+    };
+    auto b_row = [&](int j) {                              // j = (r, 8 features)
+        return (j / NT) * H2 * D2 + i2 * D2 + (j % NT) * 8 + mrow;
+    };
+
+    for (int t = 0; t < n_tiles; ++t) {
+        const int s = t % STAGES;
+        // the table entries of the tile that follows in this stage, by one warp per tile
+        const bool fetch = warp == t % WARPS && lane < TG && v0 + (t + STAGES) * TG + lane < v1;
+        int next_page = 0, next_in = 0;
+        if (fetch) {
+            int entry;
+            split_group(a.pool, tl.slot_tile(v0 + (t + STAGES) * TG + lane), entry, next_in);
+            next_page = __ldg(trow + entry);
+        }
+        if (!mbar_wait(full0 + 8 * s, (t / STAGES) & 1, a.limit_ns)) {
+            raise_error(a.p.err, kErrTimeout);
+            flags[0] = 1;
+            aborted = true;
+            break;
+        }
+        const uint32_t stage = smem_u32(smem) + s * C::STAGE_BYTES;
+        const int ng = groups_in(t), g0 = slice * CHUNKS;
+
+        // NC groups from group gi0 of the tile on, with one softmax update.  MASKED: one group
+        // with slots that the query does not see
+        auto groups = [&](auto masked_c, auto nc_c, const int gi0) {
+            constexpr bool MASKED = decltype(masked_c)::value;
+            constexpr int NC = decltype(nc_c)::value;
+            bool keep[2][2] = {{true, true}, {true, true}};        // slots 8 hf + 2c, + 1
+            if constexpr (MASKED) {
+                const int s0 = tl.slot_tile(v0 + t * TG + gi0) * 16 + 2 * c;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int sl = s0 + 8 * hf + u;
+                        keep[hf][u] = sl <= pos && (sl >= wstart || sl < a.p.mask.sinks);
+                    }
+            }
+            // ---- scores of this lane's heads, slots 2c, 2c + 1 of both halves
+            float2 sc[NC][MT][HR][2];
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                const uint32_t kgrp = stage + (gi0 + cc) * (KG + VG);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hr = 0; hr < HR; ++hr) sc[cc][mt][hr][0] = sc[cc][mt][hr][1] = make_float2(0.f, 0.f);
+                uint32_t ew[2][RK * 2 * MT];                       // A^K words: [0] of both halves when e4m3
+                if constexpr (Q8) {
+                    ldsm_list<RK * 2 * MT, false>(kgrp, lane, ew[0], a_row);
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        ldsm_list<RK * 2 * MT, false>(kgrp + hf * (C::EK * 16), lane, ew[hf], a_row);
+                }
+#pragma unroll
+                for (int r = 0; r < RK; ++r) {
+                    float acc[MT][2][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+                            acc[mt][hf][0] = acc[mt][hf][1] = acc[mt][hf][2] = acc[mt][hf][3] = 0.f;
+                    constexpr int STEP = NT >= 4 ? 4 : 2;          // matrices per load
+                    if constexpr (D2 == 8) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            // one matrix a rank: lanes 0..7 address it (the pair load takes r and r again)
+                            uint32_t bw[2];
+                            if (Q8 && hf) break;
+                            ldsm_list<2, true>(kgrp + A_K * 16 + (Q8 ? 0 : hf * (C::EK * 16)), lane, bw,
+                                               [&](int) { return b_row(r); });
+                            uint32_t b0 = bw[0], b1 = 0;
+                            if constexpr (Q8) e4m3_split(bw[0], b0, b1);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma8<Q8>(acc[mt][hf], qa[mt][0][0], qa[mt][0][1], b0);
+                                if constexpr (Q8) mma8<Q8>(acc[mt][1], qa[mt][0][0], qa[mt][0][1], b1);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int n0 = 0; n0 < NT; n0 += STEP) {
+#pragma unroll
+                            for (int hf = 0; hf < (Q8 ? 1 : 2); ++hf) {
+                                uint32_t bw[STEP];
+                                ldsm_list<STEP, true>(kgrp + A_K * 16 + hf * (C::EK * 16), lane, bw,
+                                                      [&](int j) { return b_row(r * NT + n0 + j); });
+#pragma unroll
+                                for (int k = 0; k < STEP / 2; ++k) {
+                                    if constexpr (Q8) {
+                                        uint32_t lo0, hi0, lo1, hi1;
+                                        e4m3_split(bw[2 * k], lo0, hi0);
+                                        e4m3_split(bw[2 * k + 1], lo1, hi1);
+#pragma unroll
+                                        for (int mt = 0; mt < MT; ++mt) {
+                                            mma16<true>(acc[mt][0], qa[mt][n0 / 2 + k], lo0, lo1);
+                                            mma16<true>(acc[mt][1], qa[mt][n0 / 2 + k], hi0, hi1);
+                                        }
+                                    } else {
+#pragma unroll
+                                        for (int mt = 0; mt < MT; ++mt)
+                                            mma16<false>(acc[mt][hf], qa[mt][n0 / 2 + k], bw[2 * k], bw[2 * k + 1]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int rh = 0; rh < 2; ++rh) {
+                            float2 av[2];
+                            const int j = (r * MT + mt) * 2 + rh;
+                            if constexpr (Q8) {
+                                uint32_t lo, hi;
+                                e4m3_split(ew[0][j], lo, hi);
+                                av[0] = h2_to_f2(lo);
+                                av[1] = h2_to_f2(hi);
+                            } else {
+                                av[0] = unpack_bf16x2(ew[0][j]);
+                                av[1] = unpack_bf16x2(ew[1][j]);
+                            }
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                float2 &x = sc[cc][mt][KPA ? 0 : rh][hf];
+                                x = ffma2(make_float2(acc[mt][hf][2 * rh], acc[mt][hf][2 * rh + 1]), av[hf], x);
+                            }
+                        }
+                }
+            }
+            if constexpr (KPA) {                                   // the rest of the sum over j1: lanes that differ in g & 3
+#pragma unroll
+                for (int off = 4; off <= 8; off <<= 1)
+#pragma unroll
+                    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                sc[cc][mt][0][hf].x += __shfl_xor_sync(0xffffffffu, sc[cc][mt][0][hf].x, off);
+                                sc[cc][mt][0][hf].y += __shfl_xor_sync(0xffffffffu, sc[cc][mt][0][hf].y, off);
+                            }
+            }
+            // ---- scale and mask
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                float2 ts[2] = {make_float2(a.p.qscale, a.p.qscale), make_float2(a.p.qscale, a.p.qscale)};
+                if constexpr (Q8) {
+                    const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * (KG + VG) + C::EK * 16 + 4 * c;
+                    const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
+                    // bytes: slots 2c, 2c + 8, 2c + 1, 2c + 9
+                    ts[0] = make_float2(exp_sum(s4 & 255u) * a.p.qscale, exp_sum((s4 >> 16) & 255u) * a.p.qscale);
+                    ts[1] = make_float2(exp_sum((s4 >> 8) & 255u) * a.p.qscale, exp_sum(s4 >> 24) * a.p.qscale);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hr = 0; hr < HR; ++hr)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            float2 &x = sc[cc][mt][hr][hf];
+                            x = fmul2(x, ts[hf]);
+                            if constexpr (MASKED) {
+                                if (!keep[hf][0]) x.x = -INFINITY;
+                                if (!keep[hf][1]) x.y = -INFINITY;
+                            }
+                        }
+            }
+            // ---- online softmax over the NC groups
+            bool grow = false;
+            float alpha[MT][HR];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hr = 0; hr < HR; ++hr) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int cc = 0; cc < NC; ++cc)
+                        mx = fmaxf(mx, fmaxf(fmaxf(sc[cc][mt][hr][0].x, sc[cc][mt][hr][0].y),
+                                             fmaxf(sc[cc][mt][hr][1].x, sc[cc][mt][hr][1].y)));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    alpha[mt][hr] = 1.f;
+                    if (mx > m_run[mt][hr]) {
+                        alpha[mt][hr] = ex2(m_run[mt][hr] - mx);
+                        m_run[mt][hr] = mx;
+                        grow = true;
+                    }
+                    const float m = m_run[mt][hr];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < NC; ++cc) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            sc[cc][mt][hr][hf].x = ex2(sc[cc][mt][hr][hf].x - m);
+                            sc[cc][mt][hr][hf].y = ex2(sc[cc][mt][hr][hf].y - m);
+                        }
+                        sum += (sc[cc][mt][hr][0].x + sc[cc][mt][hr][0].y) + (sc[cc][mt][hr][1].x + sc[cc][mt][hr][1].y);
+                    }
+                    l_run[mt][hr] = l_run[mt][hr] * alpha[mt][hr] + sum;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) o[mt][nt][v] *= alpha[mt][KPA ? 0 : v >> 1];
+            }
+            // ---- values
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                const uint32_t vgrp = stage + (gi0 + cc) * (KG + VG) + KG;
+                uint32_t vs[2] = {0, 0}, p2[MT][HR][2];
+                if constexpr (Q8) {
+                    const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * (KG + VG) + KG + C::EV * 16 + 4 * c;
+                    const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
+                    // 2^8 times the scales
+                    vs[0] = pack_h2(256.f * exp_sum(s4 & 255u), 256.f * exp_sum((s4 >> 16) & 255u));
+                    vs[1] = pack_h2(256.f * exp_sum((s4 >> 8) & 255u), 256.f * exp_sum(s4 >> 24));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hr = 0; hr < HR; ++hr)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf)
+                                p2[mt][hr][hf] = pack_h2(sc[cc][mt][hr][hf].x, sc[cc][mt][hr][hf].y);
+                }
+                uint32_t ew[2][RV * 2 * MT];
+                if constexpr (Q8) {
+                    ldsm_list<RV * 2 * MT, false>(vgrp, lane, ew[0], a_row);
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        ldsm_list<RV * 2 * MT, false>(vgrp + hf * (C::EV * 16), lane, ew[hf], a_row);
+                }
+#pragma unroll
+                for (int r = 0; r < RV; ++r) {
+                    uint32_t pa[MT][4];                            // P' = p A^V_r: (half, rows g / g + 8)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int rh = 0; rh < 2; ++rh) {
+                            const int j = (r * MT + mt) * 2 + rh, hr = KPA ? 0 : rh;
+                            if constexpr (Q8) {
+                                uint32_t lo, hi;
+                                e4m3_split(ew[0][j], lo, hi);
+                                pa[mt][rh] = hmul2(p2[mt][hr][0], lo);
+                                pa[mt][2 + rh] = hmul2(p2[mt][hr][1], hi);
+                            } else {
+                                const float2 x0 = fmul2(sc[cc][mt][hr][0], unpack_bf16x2(ew[0][j]));
+                                const float2 x1 = fmul2(sc[cc][mt][hr][1], unpack_bf16x2(ew[1][j]));
+                                pa[mt][rh] = pack_h2(x0.x, x0.y);
+                                pa[mt][2 + rh] = pack_h2(x1.x, x1.y);
+                            }
+                            if constexpr (MASKED) {
+                                pa[mt][rh] = mask_pair(pa[mt][rh], keep[0][0], keep[0][1]);
+                                pa[mt][2 + rh] = mask_pair(pa[mt][2 + rh], keep[1][0], keep[1][1]);
+                            }
+                        }
+                    constexpr int STEP = Q8 ? (NT >= 4 ? 4 : 2) : (NT >= 2 ? 2 : 1);   // 8-feature blocks per load
+#pragma unroll
+                    for (int n0 = 0; n0 < NT; n0 += STEP) {
+                        uint32_t b0[STEP], b1[STEP];
+                        if constexpr (Q8) {
+                            uint32_t bw[STEP];
+                            ldsm_list<STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
+                                return b_row(r * NT + (NT == 1 ? 0 : n0 + j));
+                            });
+#pragma unroll
+                            for (int k = 0; k < STEP; ++k) {
+                                e4m3_split(bw[k], b0[k], b1[k]);
+                                b0[k] = hmul2(b0[k], vs[0]);
+                                b1[k] = hmul2(b1[k], vs[1]);
+                            }
+                        } else {
+                            // matrices (block, half): half 1 lies one 8-slot group further
+                            uint32_t bw[2 * STEP];
+                            ldsm_list<2 * STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
+                                return b_row(r * NT + n0 + (j >> 1)) + (j & 1) * C::EV;
+                            });
+#pragma unroll
+                            for (int k = 0; k < STEP; ++k) {
+                                b0[k] = bf16x2_to_h2(bw[2 * k]);
+                                b1[k] = bf16x2_to_h2(bw[2 * k + 1]);
+                            }
+                        }
+                        if constexpr (MASKED) {
+#pragma unroll
+                            for (int k = 0; k < STEP; ++k) {
+                                b0[k] = mask_pair(b0[k], keep[0][0], keep[0][1]);
+                                b1[k] = mask_pair(b1[k], keep[1][0], keep[1][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < STEP; ++k)
+                            if (n0 + k < NT) {
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) mma16<true>(o[mt][n0 + k < NT ? n0 + k : 0], pa[mt], b0[k], b1[k]);
+                            }
+                    }
+                }
+            }
+        };
+        // does group i of the tile hold slots that the query does not see?
+        auto partial = [&](int i) {
+            const int s0 = tl.slot_tile(v0 + t * TG + i) * 16;
+            return s0 + 15 > pos || (s0 < wstart && s0 + 15 >= a.p.mask.sinks);
+        };
+        bool whole = g0 + CHUNKS <= ng;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) whole = whole && !partial(g0 + i);
+        if (whole) {
+            groups(std::false_type{}, std::integral_constant<int, CHUNKS>{}, g0);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < CHUNKS && g0 + i < ng; ++i) {
+                if (CHUNKS == 1 || partial(g0 + i))
+                    groups(std::true_type{}, std::integral_constant<int, 1>{}, g0 + i);
+                else if constexpr (CHUNKS > 1)
+                    groups(std::false_type{}, std::integral_constant<int, 1>{}, g0 + i);
+            }
+        }
+        if (fetch) tab[s * TG + lane] = group_index(next_page, next_in);
+        __syncwarp();
+        // the last warp to release stage s issues tile t + STAGES into it (acq_rel: every
+        // warp's reads of the stage, and the table entries, come first)
+        uint32_t last = 0;
+        if (lane == 0) {
+            uint32_t old;
+            asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+                         : "=r"(old)
+                         : "r"(smem_u32((const void *)(flags + 1 + s)))
+                         : "memory");
+            last = (old + 1) % WARPS == 0 && t + STAGES < n_tiles && !flags[0];
+            if (last) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_expect_tx(full0 + 8 * s, groups_in(t + STAGES) * (KG + VG));
+            }
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();                                       // lane 0's acquire covers the warp
+        if (last) {
+            if (lane < groups_in(t + STAGES)) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                copy_group(s, lane, tab[s * TG + lane]);
+            }
+            __syncwarp();
+        }
+        if (flags[0]) { aborted = true; break; }
+    }
+    __syncthreads();
+    if (aborted || flags[0]) {                              // copies still in flight land before the CTA ends
+        if (tid == 0)
+            for (int t = max(0, n_tiles - STAGES); t < n_tiles; ++t)
+                (void)mbar_wait(full0 + 8 * (t % STAGES), (t / STAGES) & 1, a.limit_ns);
+        __syncthreads();
+        return;
+    }
+
+    // ---- the sum of each head over its lanes, then the merge of the token slices
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hr = 0; hr < HR; ++hr) {
+            l_run[mt][hr] += __shfl_xor_sync(0xffffffffu, l_run[mt][hr], 1);
+            l_run[mt][hr] += __shfl_xor_sync(0xffffffffu, l_run[mt][hr], 2);
+        }
+    float *mo = reinterpret_cast<float *>(smem), *mm = mo + SLICES * H * C::MO_LD;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+            const int head = KPA ? (2 * mt + (g >> 2)) * H2 + i2 : (hs * MT + mt) * 16 + g + 8 * rh;
+            const int j1 = KPA ? 2 * (g & 3) + rh : 0, hr = KPA ? 0 : rh;
+            float *dst = mo + (size_t)(slice * H + head) * C::MO_LD + j1 * D2;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                *reinterpret_cast<float2 *>(dst + nt * 8 + 2 * c) = make_float2(o[mt][nt][2 * rh], o[mt][nt][2 * rh + 1]);
+            if (c == 0 && (!KPA || ((g & 3) == 0 && rh == 0)))
+                *reinterpret_cast<float2 *>(mm + (slice * H + head) * 2) = make_float2(m_run[mt][hr], l_run[mt][hr]);
+        }
+    __syncthreads();
+    constexpr float kBack = Q8 ? 1.f / 256.f : 1.f;
+    bool finite = true;
+    for (int i4 = tid; i4 < H * DH / 4; i4 += C::THREADS) {
+        const int head = i4 * 4 / DH, col = i4 * 4 % DH;
+        float M = -INFINITY;
+#pragma unroll
+        for (int sl = 0; sl < SLICES; ++sl) M = fmaxf(M, mm[(sl * H + head) * 2]);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int sl = 0; sl < SLICES; ++sl) {
+            const float2 ms = *reinterpret_cast<const float2 *>(mm + (sl * H + head) * 2);
+            if (ms.x == -INFINITY && ms.y == 0.f) continue;         // a slice without a group
+            const float w = exp2f(ms.x - M);
+            const float4 v = *reinterpret_cast<const float4 *>(mo + (size_t)(sl * H + head) * C::MO_LD + col);
+            l += w * ms.y;
+            acc.x += w * v.x;
+            acc.y += w * v.y;
+            acc.z += w * v.z;
+            acc.w += w * v.w;
+        }
+        const float f = a.p.n_split == 1 ? (l == 0.f ? 0.f : a.p.out_scale * kBack / l) : kBack;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        finite = finite && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w) && l <= 3.4e38f;
+        if (a.p.n_split == 1) {
+            __nv_bfloat162 w2[2] = {__floats2bfloat162_rn(acc.x, acc.y), __floats2bfloat162_rn(acc.z, acc.w)};
+            *reinterpret_cast<uint2 *>(a.p.out + (size_t)b * H * DH + i4 * 4) = *reinterpret_cast<const uint2 *>(w2);
+        } else {
+            const size_t at = (size_t)(b * H + head) * a.p.n_split + split;
+            *reinterpret_cast<float4 *>(a.p.part_o + at * DH + col) = acc;
+            if (col == 0) *reinterpret_cast<float2 *>(a.p.part_ml + at * 2) = make_float2(M, l);
+        }
+    }
+    // a cached value that is not finite, or an operand outside the fp16 range
+    if (!finite) raise_error(a.p.err, kErrDeviceCheck);
+}
+
+// (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools)
+#define KPA_PAGED_DECODE_VARIANTS(X)            \
+    X(0, 16, 1, 64, 2, 2, 1, 1, 8, 1, 2, 8, 2, 2)    \
+    X(1, 32, 8, 16, 4, 4, 8, 1, 2, 1, 2, 2, 2, 2)    \
+    X(2, 32, 8, 16, 2, 2, 8, 1, 2, 2, 2, 2, 2, 4)    \
+    X(3, 32, 8, 16, 2, 2, 4, 1, 4, 1, 2, 4, 2, 2)    \
+    X(4, 32, 1, 64, 1, 1, 1, 2, 4, 4, 2, 8, 2, 2)    \
+    X(5, 32, 8, 8, 2, 2, 4, 1, 4, 2, 2, 4, 2, 2)     \
+    X(6, 16, 8, 8, 2, 2, 8, 1, 2, 2, 2, 2, 2, 4)     \
+    X(7, 64, 8, 8, 2, 2, 2, 1, 8, 1, 2, 8, 1, 2)     \
+    X(8, 16, 1, 128, 2, 2, 1, 1, 4, 1, 2, 8, 1, 2)   \
+    X(9, 32, 8, 16, 4, 4, 4, 1, 4, 1, 2, 4, 1, 4)
+
+template <class C>
+cudaError_t launch_cfg(const DecodeArgsP &a, cudaStream_t st) {
+    cudaError_t e = ensure_dynamic_smem<paged_decode_kernel<C>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)a.p.n_split, (unsigned)a.p.batch);
+    lc.blockDim = dim3(C::THREADS);
+    lc.dynamicSmemBytes = C::SMEM;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, paged_decode_kernel<C>, a);
+}
+
+}  // namespace
+
+int paged_decode_variant(const Dims &d) {
+#define KPA_MATCH(IDX, MA, D1, D2, RK, RV, H2, HS, ...) \
+    if (d.h1 * d.d1 == MA && d.d1 == D1 && d.d2 == D2 && d.rk == RK && d.rv == RV && d.h2 == H2) return IDX;
+    KPA_PAGED_DECODE_VARIANTS(KPA_MATCH)
+#undef KPA_MATCH
+    return -1;
+}
+
+void paged_decode_shape(int variant, bool e4m3, int *tile_groups, int *ctas_per_sm) {
+    size_t smem = 1;
+    int threads = 1;
+    switch (variant) {
+#define KPA_SHAPE(IDX, MA, D1, D2, RK, RV, H2, HS, S0, C0, T0, S1, C1, T1)          \
+    case IDX:                                                                        \
+        if (e4m3) {                                                                  \
+            using C = Cfg<MA, D1, D2, RK, RV, H2, S1, HS, C1, T1, true>;             \
+            *tile_groups = C::TG, smem = C::SMEM, threads = C::THREADS;              \
+        } else {                                                                     \
+            using C = Cfg<MA, D1, D2, RK, RV, H2, S0, HS, C0, T0, false>;            \
+            *tile_groups = C::TG, smem = C::SMEM, threads = C::THREADS;              \
+        }                                                                            \
+        break;
+        KPA_PAGED_DECODE_VARIANTS(KPA_SHAPE)
+#undef KPA_SHAPE
+        default:
+            *tile_groups = 1;
+    }
+    // 1 KB of shared memory a CTA is the system's; a warp holds up to 128 registers a thread
+    const int by_smem = (int)(228 * 1024 / (smem + 1024)), by_warps = 512 / threads;
+    *ctas_per_sm = by_smem < by_warps ? by_smem : by_warps;
+    if (*ctas_per_sm < 1) *ctas_per_sm = 1;
+}
+
+cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &p, int groups_per_split,
+                                unsigned long long wait_limit_ns, cudaStream_t st) {
+    DecodeArgsP a;
+    a.p = p;
+    a.pool = s.pool;
+    a.gps = groups_per_split;
+    a.limit_ns = wait_limit_ns;
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (variant) {
+#define KPA_CASE(IDX, MA, D1, D2, RK, RV, H2, HS, S0, C0, T0, S1, C1, T1)                              \
+    case IDX:                                                                                           \
+        e = s.pool.e4m3 ? launch_cfg<Cfg<MA, D1, D2, RK, RV, H2, S1, HS, C1, T1, true>>(a, st)          \
+                        : launch_cfg<Cfg<MA, D1, D2, RK, RV, H2, S0, HS, C0, T0, false>>(a, st);        \
+        break;
+        KPA_PAGED_DECODE_VARIANTS(KPA_CASE)
+#undef KPA_CASE
+    }
+    if (e != cudaSuccess || p.n_split == 1) return e;
+    return launch_paged_combine(s, p, st);
+}
+
+}  // namespace kpa

@@ -483,12 +483,17 @@ int smem_bytes(const Dims &d, bool e4m3) {
 }
 
 // out[row][head] = out_scale * sum_z 2^(m_z - M) o_z / sum_z 2^(m_z - M) l_z over the splits of
-// a row: one warp per (row, head); a split that saw nothing (m = -inf) is not read.
+// a row; a split that saw nothing (m = -inf, l = 0) is not read.  W warps share a (row, head):
+// one when there are few splits, eight (a whole block) when there are many, so that the loads
+// of a long list run side by side.
+template <int W>
 __global__ void __launch_bounds__(256) paged_combine_kernel(PagedAttnArgs a, int h, int dh) {
+    __shared__ float part[8][128 + 1];                              // features, then l
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long rh = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long rh = (long long)blockIdx.x * (8 / W) + warp / W;
     if (rh >= (long long)a.n_rows * h) return;
-    const int row = (int)(rh / h), lane = threadIdx.x & 31;
+    const int row = (int)(rh / h);
     if (a.cu && (row < a.cu[0] || row >= a.cu[a.batch])) return;    // a row of no sequence
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + rh * a.n_split;
     const float *po = a.part_o + rh * a.n_split * dh;
@@ -498,7 +503,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(PagedAttnArgs a, int
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float l = 0.f;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};                            // features lane + 32 i
-    for (int z = 0; z < a.n_split; ++z) {
+#pragma unroll 4
+    for (int z = warp % W; z < a.n_split; z += W) {
         const float2 s = ml[z];
         if (s.x == -INFINITY && s.y == 0.f) continue;
         const float w = exp2f(s.x - M);
@@ -506,6 +512,19 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(PagedAttnArgs a, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (lane + 32 * i < dh) acc[i] += w * po[(long long)z * dh + lane + 32 * i];
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][lane + 32 * i] = acc[i];
+        if (lane == 0) part[warp][128] = l;
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] += part[w][lane + 32 * i];
+            l += part[w][128];
+        }
     }
     const float inv = l == 0.f ? 0.f : a.out_scale / l;
 #pragma unroll
@@ -523,9 +542,10 @@ bool paged_mma_supported(const Dims &d, bool e4m3) {
 }
 
 cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st) {
-    const long long warps = (long long)a.n_rows * s.d.h;
+    const long long rh = (long long)a.n_rows * s.d.h;
+    const bool wide = a.n_split > 8;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)((warps + 7) / 8));
+    lc.gridDim = dim3((unsigned)(wide ? rh : (rh + 7) / 8));
     lc.blockDim = dim3(256);
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -533,7 +553,8 @@ cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, paged_combine_kernel, a, s.d.h, s.d.dh);
+    return wide ? cudaLaunchKernelEx(&lc, paged_combine_kernel<8>, a, s.d.h, s.d.dh)
+                : cudaLaunchKernelEx(&lc, paged_combine_kernel<1>, a, s.d.h, s.d.dh);
 }
 
 namespace {

@@ -422,7 +422,9 @@ kpa_status kpa_paged_prefill(const kpa_config *cfg, const kpa_pages *pages, int3
                              size_t ws_bytes, kpa_stream stream);
 
 /* The same attention for one token per sequence: the query is at position seq_len[b] - 1,
- * the newest slot.
+ * the newest slot.  The splits with a kernel of their own (kpa_paged_decode_kernel_kind)
+ * never form K and V: scores are fp32 sums of exact products, and the weighted value
+ * factors p A^V (over an e4m3 pool the weights p first) are rounded to fp16.
  *   q    [batch][h][d_h]  bf16, already rotated
  *   seq_len [batch] int32  0 <= seq_len[b] <= max_len; a longer length is clamped to
  *        max_len, a negative one to 0, and sets KPA_ERR_DEVICE_CHECK; 0 gives zeros
@@ -434,6 +436,15 @@ kpa_status kpa_paged_decode(const kpa_config *cfg, const kpa_pages *pages, int32
                             const int32_t *seq_len, const int32_t *page_table, const void *kpool, const void *vpool,
                             int32_t max_len, int32_t window, int32_t sinks, float sm_scale, void *out,
                             void *workspace, size_t ws_bytes, kpa_stream stream);
+
+/* Which kernel kpa_paged_decode and kpa_paged_prefill run for a config and pool:
+ *   KPA_PAGED_KERNEL_CHUNKS   the mma.sync kernel that rebuilds K and V, for every split
+ *   KPA_PAGED_KERNEL_FACTORS  (decode) the tensor-core kernel on the factors
+ *   KPA_PAGED_KERNEL_TCGEN05  (prefill) the tcgen05 kernel that rebuilds K and V
+ * Same argument rules as kpa_paged_page_bytes. */
+enum { KPA_PAGED_KERNEL_CHUNKS = 0, KPA_PAGED_KERNEL_FACTORS = 1, KPA_PAGED_KERNEL_TCGEN05 = 2 };
+kpa_status kpa_paged_decode_kernel_kind(const kpa_config *cfg, const kpa_pages *pages, int32_t *kind);
+kpa_status kpa_paged_prefill_kernel_kind(const kpa_config *cfg, const kpa_pages *pages, int32_t *kind);
 
 /* Upper bound, in bytes, of the scratch that kpa_decode_noalloc can use. */
 #define KPA_DECODE_NOALLOC_MAX_BYTES (16u << 20)

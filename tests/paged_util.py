@@ -108,6 +108,11 @@ def dense(x, s, r):
     return (np.einsum("nrxi,nryj->nxyij", a, b) / r).reshape(n, s.h, s.dh)
 
 
+def dense_abs(x, s, r):
+    """[n][h][d_h] of (1/R) sum_r |A_r| (x) |B_r|."""
+    return dense(np.abs(x), s, r)
+
+
 def visible(p, n, window, sinks):
     t = np.arange(n)
     see = t <= p
@@ -157,7 +162,7 @@ class Cache:
         return lib.make_pages(self.page, self.n_pages, self.stride, self.fmt)
 
 
-def attention(c, b, q, pos, window, sinks, scale, k=None, v=None):
+def attention(c, b, q, pos, window, sinks, scale, k=None, v=None, factored=False):
     """Rows q [n][h][d_h] (float64) at positions pos [n] of sequence b: out and the bound on the
     GPU's distance from it.
 
@@ -165,7 +170,12 @@ def attention(c, b, q, pos, window, sinks, scale, k=None, v=None):
     2^-25 where the result is below fp16's normal range) and the output once to bf16 (2^-8); a
     key that is formed from rounded factors may carry two roundings.  A score is then off by at
     most d = 2^-11 * 3 * sum |q||K| scale + 2^-25 (sum |K| + sum |q| scale) (log2 e times that, in
-    base 2), each weight by a factor within e^(2 d), and the rest is linear."""
+    base 2), each weight by a factor within e^(2 d), and the rest is linear: the weights' and the
+    values' roundings together move an output by at most 2 * 2^-11 * sum p |V|.
+
+    factored: the single-token kernel never forms V.  It rounds each weighted factor p A^V_r to
+    fp16 (over an e4m3 pool the weight first), so its error is 2 * 2^-11 * sum_s p sum_r |A_r||B_r|
+    / R, where ranks that cancel in V do not cancel: sum p |V| is replaced by that sum."""
     s = c.s
     out = np.zeros((len(q), s.h, s.dh))
     tol = np.zeros_like(out)
@@ -181,7 +191,7 @@ def attention(c, b, q, pos, window, sinks, scale, k=None, v=None):
         size = np.einsum("hd,nhd->hn", np.abs(q[i]), np.abs(K)).max(1) * abs(scale)
         sub = np.abs(K).sum(2).max(0) + np.abs(q[i]).sum(1) * abs(scale)
         d = 3 * 2.0 ** -11 * size + 2.0 ** -25 * sub + 2.0 ** -20 * (1 + np.abs(z).max(1))
-        va = np.einsum("hn,nhd->hd", w, np.abs(V))
+        va = np.einsum("hn,nhd->hd", w, dense_abs(vx, s, s.r_v) if factored else np.abs(V))
         tol[i] = (2.0 ** -8 * np.abs(out[i]) + va * (np.expm1(2 * d) + 4 * 2.0 ** -11)[:, None]
                   + 2.0 ** -25 * (1 + len(slots) * np.abs(V).max((0, 2)))[:, None])
     return out, tol
