@@ -180,6 +180,12 @@ int paged_mma_rows();                                        // rows of a tile
 cudaError_t launch_paged_mma(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 
+// The tcgen05 chunk kernel (d1 = 8): whether it takes this shape and pool, and its launcher.
+bool paged_prefill_supported(const PagedShape &s);
+int paged_prefill_rows();                                    // rows of a tile
+cudaError_t launch_paged_prefill(const PagedShape &s, const PagedAttnArgs &a, unsigned long long wait_limit_ns,
+                                 cudaStream_t st);
+
 // The single-token kernel: its variant for these dims (-1: none, the chunk kernel takes
 // them), the 16-slot groups of its tiles and its CTAs per SM, and its launcher.
 int paged_decode_variant(const Dims &d);

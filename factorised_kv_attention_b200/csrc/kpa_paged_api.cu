@@ -42,16 +42,17 @@ kpa_status check_paged(const kpa_config *cfg, const kpa_pages *pg, PagedShape *s
 }
 
 struct AttnPlan {
-    int variant;                 // of the single-token kernel, or -1: the chunk kernel
+    int variant;                 // of the single-token kernel, or -1: a chunk kernel
+    bool tcgen05;                // (chunk kernels) the tcgen05 one
     int groups_per_split;        // (single-token kernel)
     int n_split;
     size_t ml_off, bytes;
 };
 
 // How the rows' key range is split.
-//  - The chunk kernel: when there are fewer CTAs than two per SM, into as many runs as make
-//    up for it, of at least four tiles (256 slots) each: shorter ones cost more in partials
-//    than they gain.
+//  - The chunk kernels: when there are fewer CTAs than two per SM, into as many runs as make
+//    up for it, of at least four tiles each: shorter ones cost more in partials than they
+//    gain.
 //  - The single-token kernel: one CTA per slot of the SMs for a single sequence; several
 //    sequences may have different lengths (the host does not see them), so up to four times
 //    as many shorter runs let the CTA scheduler even them out, as long as a run keeps eight
@@ -62,7 +63,8 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
     const bool e4m3 = ps.pool.e4m3 != 0;
     AttnPlan p = {};
     p.variant = chunks ? -1 : paged_decode_variant(d);
-    const int tr = paged_mma_rows();
+    p.tcgen05 = chunks && paged_prefill_supported(ps);
+    const int tr = p.tcgen05 ? paged_prefill_rows() : paged_mma_rows();
     auto visible = [&](int64_t T, int64_t rows) {          // units of T slots that a set of rows sees at most
         const int64_t all = ((int64_t)max_len + T - 1) / T;
         return window > 0 ? std::min(all, ((int64_t)sinks + T - 1) / T + ((int64_t)window + rows) / T + 2) : all;
@@ -84,7 +86,8 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         p.groups_per_split = (int)(per * tg);
         p.n_split = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
     } else {
-        constexpr int kTile = 64, kMinTiles = 4;
+        constexpr int kMinTiles = 4;
+        const int kTile = p.tcgen05 ? 128 : 64;
         const int64_t row_tiles = chunks ? std::max<int64_t>((n_rows + tr - 1) / tr, std::min(batch, n_rows)) : batch;
         const int64_t ctas = std::max<int64_t>(1, row_tiles * d.h);
         const int64_t s =
@@ -171,7 +174,8 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
     a.err = err;
     const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split,
                                                                device_wait_limit_ns(), (cudaStream_t)stream)
-                                         : launch_paged_mma(s, a, (cudaStream_t)stream);
+                          : p.tcgen05      ? launch_paged_prefill(s, a, device_wait_limit_ns(), (cudaStream_t)stream)
+                                           : launch_paged_mma(s, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KPA_OK : fail(e);
 }
 
@@ -262,7 +266,9 @@ static kpa_status kernel_kind(const kpa_config *cfg, const kpa_pages *pages, boo
     if (st != KPA_OK) return st;
     if (!kind) return KPA_ERR_INVALID_ARG;
     if (!paged_mma_supported(s.d, s.pool.e4m3 != 0)) return KPA_ERR_UNSUPPORTED;
-    *kind = !chunks && paged_decode_variant(s.d) >= 0 ? KPA_PAGED_KERNEL_FACTORS : KPA_PAGED_KERNEL_CHUNKS;
+    *kind = KPA_PAGED_KERNEL_CHUNKS;
+    if (!chunks && paged_decode_variant(s.d) >= 0) *kind = KPA_PAGED_KERNEL_FACTORS;
+    if (chunks && paged_prefill_supported(s)) *kind = KPA_PAGED_KERNEL_TCGEN05;
     return KPA_OK;
 }
 

@@ -1,0 +1,693 @@
+// kpa_paged_prefill.cu -- attention of chunks of new tokens over a paged factor cache on the
+// tcgen05 tensor cores, for d1 = 8 (d2 = 16 at R = 2 or 4, d2 = 8 at R = 2); every other
+// split runs on the mma.sync kernel.
+//
+// The arrangement is the contiguous cache's prefill: one CTA takes 256 query rows of one
+// (sequence, head) as two 128-row halves that share every rebuilt 128-slot K/V tile and take
+// turns on the tensor pipe; a producer warp streams factor slices with TMA, eight warps
+// rebuild K and V^T as fp16 in the 128-byte-swizzled layouts tcgen05.mma reads, one thread
+// issues S_h = Q_h K^T and O_h += P_h V, and eight softmax warps (a row per thread) turn S_h
+// into P_h in tensor memory (S0 | S1 | O0 | O1, 128 columns each).  What differs:
+//   - rows come flattened, each CTA finds its sequence by a scan of the row offsets;
+//   - the tiles are those the CTA's rows see: the sinks' and the windows', or one of n_split
+//     equal runs of them when there are few CTAs, whose partials a second kernel joins;
+//   - a tile's 16-slot groups come through the page table: the producer's lanes each load
+//     boxes of as many groups as a page surely holds together (1, 2, 4 or 8), and skip boxes
+//     that no row sees; rebuilt slots that no row sees are zeros;
+//   - an e4m3 token's two scales multiply into its A factors, in fp32, before K and V are
+//     rounded once to fp16.
+#include <cstring>
+
+#include "kpa_f32x2.cuh"
+#include "kpa_paged.cuh"
+#include "kpa_prefill_tc.cuh"
+
+namespace kpa {
+namespace {
+
+using namespace paged;
+using namespace prefill_tc;
+using f32x2::exp2_poly2;
+using f32x2::fadd2;
+using f32x2::ffma2;
+using f32x2::fmul2;
+using f32x2::fsub2;
+using f32x2::unpack_bf16x2;
+
+constexpr int HQ = 128;                       // query rows per half
+constexpr int TK = 128;                       // slots per tile
+constexpr int kSoftmaxWarps = 8, kRebuildWarps = 8;
+constexpr int kRebuildWarp0 = kSoftmaxWarps;
+constexpr int kMmaWarp = kSoftmaxWarps + kRebuildWarps;
+constexpr int kProducerWarp = kMmaWarp + 1;
+constexpr int kThreads = (kProducerWarp + 1) * 32;            // 576
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;           // the running maximum moves when it grew past 2^8
+
+struct PrefillArgsP {
+    PagedAttnArgs p;
+    Pool pool;
+    int h1, h2;
+    int box_groups;                           // 16-slot groups per TMA box: 1, 2, 4 or 8
+    unsigned long long wait_limit_ns;
+};
+
+template <int D2_, int R_, bool E4M3_>
+struct Cfg {
+    static constexpr int D1 = 8, D2 = D2_, R = R_, DH = D1 * D2, HB = D2 / 8;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int NG = E4M3 ? TK / 16 : TK / 8;         // layout groups of a tile
+    static constexpr int BOX = NG * 128;                       // 8 elements x the tile's slots
+    static constexpr int NBLK = R * (1 + HB);                  // blocks of a plane: A_r, then (r, hb) of B
+    static constexpr int FACT = NBLK * BOX;                    // bytes of a stage, then 32 scale bytes a group
+    static constexpr int ST = FACT + (E4M3 ? NG * 32 : 0);
+    // factor stages: two where they fit beside the Q, K and V tiles, else one
+    static constexpr int FST = 2 * 2 * ST <= 56 * 1024 ? 2 : 1;
+    static constexpr uint32_t Q_HALF = HQ * DH * 2, KV_TILE = TK * DH * 2;
+    static constexpr size_t OFF_Q = 0;                         // two halves
+    static constexpr size_t OFF_K = OFF_Q + 2 * Q_HALF;        // two buffers
+    static constexpr size_t OFF_V = OFF_K + 2 * KV_TILE;       // one buffer
+    static constexpr size_t OFF_KST = OFF_V + KV_TILE;
+    static constexpr size_t OFF_VST = OFF_KST + (size_t)FST * ST;
+    static constexpr size_t OFF_BAR = OFF_VST + (size_t)FST * ST;
+    static constexpr int NBAR = 24;
+    static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
+    static_assert(D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
+    static_assert(ST % 128 == 0 && SMEM <= 226 * 1024, "shared memory (a little is static)");
+};
+
+// mbarrier slots
+enum : int {
+    B_Q = 0,
+    B_QREADY = 1,      // +h
+    B_KST_FULL = 3,    // +stage
+    B_VST_FULL = 5,
+    B_KST_EMPTY = 7,
+    B_VST_EMPTY = 9,
+    B_K_FULL = 11,     // +buffer
+    B_K_EMPTY = 13,
+    B_V_FULL = 15,
+    B_V_EMPTY = 16,
+    B_S_FULL = 17,     // +h
+    B_P_FULL = 19,     // +h
+    B_O_FINAL = 21,    // +h
+    B_DRAIN = 23,
+};
+
+// Which local tiles a half works on: both start at 0; half h stops at last[h].
+struct TilePlan {
+    bool act[2];
+    int last[2];
+    int n_kt;
+    __device__ bool active(int h, int t) const { return act[h] && t <= last[h]; }
+    __device__ int first_half(int t) const { return active(0, t) ? 0 : 1; }
+    __device__ int last_half(int t) const { return active(1, t) ? 1 : 0; }
+};
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgsP a) {
+    constexpr int D1 = C::D1, R = C::R, DH = C::DH, HB = C::HB;
+    constexpr bool E4M3 = C::E4M3;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t bar0 = smem_u32(smem + C::OFF_BAR);
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + C::NBAR * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.y, split = blockIdx.z;
+    const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
+    const uint64_t limit = a.wait_limit_ns;
+
+    // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r; the last rows of a
+    // sequence, which see most, first
+    const Found f = find_unit<kThreads>(blockIdx.x, a.p.batch, blockIdx.x == 0, [&](int s) {
+        int r0, r1;
+        if (!rows_of(a.p.cu, s, a.p.n_rows, r0, r1)) {
+            if (blockIdx.x == 0) raise_error(a.p.err, kErrDeviceCheck);
+            return 0;
+        }
+        return (r1 - r0 + 2 * HQ - 1) / (2 * HQ);
+    });
+    if (f.b < 0) return;
+    const int b = f.b, seq0 = a.p.cu[b], seq_n = a.p.cu[b + 1] - seq0;
+    const int q0 = ((seq_n + 2 * HQ - 1) / (2 * HQ) - 1 - f.i) * 2 * HQ;
+    const int row0 = seq0 + q0, n = min(2 * HQ, seq_n - q0);
+    const long long pos0 = (long long)a.p.start[b] + q0;
+    if (tid == 0 && (pos0 < 0 || pos0 + n > a.p.max_len)) raise_error(a.p.err, kErrDeviceCheck);
+
+    // ---- tiles: what the rows with a position in [0, max_len) see
+    const int lo = (int)max(pos0, 0ll), hi = (int)min(pos0 + n - 1, (long long)a.p.max_len - 1);
+    Tiles tl = {0, 0, 0};
+    if (lo <= hi) tl = visible_tiles(a.p.mask, lo, hi, TK);
+    const int wstart = lo <= hi ? window_start(a.p.mask, lo) : 0;
+    const int v0 = (int)((long long)tl.n * split / a.p.n_split), v1 = (int)((long long)tl.n * (split + 1) / a.p.n_split);
+    TilePlan tp;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        const long long plo = max(pos0 + hh * HQ, 0ll);
+        const long long phi = min(pos0 + min(n, (hh + 1) * HQ) - 1, (long long)a.p.max_len - 1);
+        tp.act[hh] = hh * HQ < n && plo <= phi;
+        tp.last[hh] = tp.act[hh] ? min((int)(phi / TK) - tl.gap, v1 - 1) - v0 : -1;
+        if (tp.last[hh] < 0) tp.act[hh] = false, tp.last[hh] = -1;
+    }
+    tp.n_kt = max(tp.last[0], tp.last[1]) + 1;
+    auto seen = [&](int s) { return s <= hi && (s >= wstart || s < a.p.mask.sinks); };
+
+    if (tid == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            uint32_t count = 1;
+            if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2)) count = 4;
+            if ((i >= B_KST_EMPTY && i < B_KST_EMPTY + 2) || (i >= B_VST_EMPTY && i < B_VST_EMPTY + 2) ||
+                (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL)
+                count = kRebuildWarps;
+            mbar_init(bar(i), count);
+        }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // Bounded wait shared by every role: gives up when the time runs out or another thread has
+    // already given up, and records the timeout once.
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar(i), parity)) return true;
+        const uint64_t t0 = globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar(i), parity)) return true;
+            if ((it & 15) == 0) {
+                if (*abort_flag) return false;
+                if (globaltimer() - t0 > limit) {
+                    *abort_flag = 1;
+                    raise_error(a.p.err, kErrTimeout);
+                    return false;
+                }
+            }
+        }
+    };
+
+    if (warp == kProducerWarp) {
+        // ---------------------------------------------------------------- producer
+        if (tp.n_kt > 0) {
+            if (lane == 0) {
+                tma_prefetch_desc(&tmq);
+                tma_prefetch_desc(&tmk);
+                tma_prefetch_desc(&tmv);
+            }
+            const int bg = a.box_groups, nb = TK / 16 / bg;       // boxes of a tile
+            const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
+            // lane i < nb: the first 16-slot group of box i of local tile t (-1: seen by no row)
+            auto lookup = [&](int t) -> long long {
+                if (lane >= nb || t >= tp.n_kt) return -1;
+                const int s0 = tl.slot_tile(v0 + t) * TK + lane * bg * 16;
+                if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return -1;
+                int entry, in;
+                split_group(a.pool, s0 >> 4, entry, in);
+                int page = __ldg(trow + entry);
+                if (page < 0 || page >= a.pool.n_pages) {
+                    raise_error(a.p.err, kErrDeviceCheck);
+                    page = 0;
+                }
+                return (long long)page * a.pool.pg + in;
+            };
+            const int ab = R * a.h1 * D1;                         // first B element of a record
+            int issued[2][2] = {{-1, -1}, {-1, -1}};              // [plane][stage]
+            auto issue = [&](int t, bool is_v, long long grp) -> bool {
+                const int s = t % C::FST;
+                const bool ok = !(t >= C::FST) || wait((is_v ? B_VST_EMPTY : B_KST_EMPTY) + s, ((t / C::FST) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                const uint32_t full = bar((is_v ? B_VST_FULL : B_KST_FULL) + s);
+                const uint32_t st = smem_u32(smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
+                const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
+                const int rows = E4M3 ? bg : 2 * bg;              // layout groups of a box
+                if (lane == 0)
+                    mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
+                __syncwarp();
+                const CUtensorMap *map = is_v ? &tmv : &tmk;
+                for (int i = lane; i < ((C::NBLK * nb + 31) & ~31); i += 32) {
+                    const int box = i % nb, k = i / nb;
+                    const long long g = __shfl_sync(0xffffffffu, grp, box);
+                    if (g < 0 || k >= C::NBLK) continue;
+                    const int e = k < R ? k * a.h1 * D1 + i1 * D1
+                                        : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8;
+                    tma_load_2d(st + k * C::BOX + box * rows * 128, map, e * 4, (int)(E4M3 ? g : 2 * g), full);
+                }
+                if constexpr (E4M3) {                             // the two scale rows of each group
+                    const long long g = __shfl_sync(0xffffffffu, grp, (lane & 7) / bg);
+                    if (lane < 8 && g >= 0) {
+                        const int gb = is_v ? a.pool.vg : a.pool.kg;
+                        const unsigned char *src =
+                            (is_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
+                        sm100::bulk_g2s(st + C::FACT + lane * 32, src, 32, full);
+                    }
+                }
+                issued[is_v ? 1 : 0][s] = t;
+                return true;
+            };
+            long long grp = lookup(0);
+            // the first key tile's factors go out ahead of Q: its rebuild is the first step
+            bool ok = issue(0, false, grp);
+            const int nh = (tp.act[0] ? 1 : 0) + (tp.act[1] ? 1 : 0);
+            if (lane == 0) {
+                mbar_expect_tx(bar(B_Q), (uint32_t)nh * C::Q_HALF);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    if (tp.act[hh])
+#pragma unroll
+                        for (int cb = 0; cb < DH / 64; ++cb)
+                            tma_load_2d(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + cb * HQ * 128), &tmq,
+                                        head * DH + cb * 64, row0 + hh * HQ, bar(B_Q));
+            }
+            __syncwarp();
+            long long next = lookup(1);
+            if (ok) ok = issue(0, true, grp);
+            for (int t = 1; t < tp.n_kt && ok; ++t) {
+                grp = next;
+                next = lookup(t + 1);
+                ok = issue(t, false, grp);
+                if (ok) ok = issue(t, true, grp);
+            }
+            // every copy this warp started lands before the CTA can exit
+            (void)mbar_wait(bar(B_Q), 0, limit);
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+                for (int s = 0; s < C::FST; ++s)
+                    if (issued[pl][s] >= 0)
+                        (void)mbar_wait(bar((pl ? B_VST_FULL : B_KST_FULL) + s), (issued[pl][s] / C::FST) & 1, limit);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA issue
+        if (lane == 0 && tp.n_kt > 0) {
+            const uint32_t idesc_s = umma_idesc_f16_f32(HQ, TK), idesc_o = umma_idesc_f16_f32(HQ, DH);
+            bool ok = true;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+                if (ok && tp.act[hh] && !wait(B_QREADY + hh, 0)) ok = false;
+            auto issue_s = [&](int hh, int t) -> bool {
+                const int kb = t & 1;
+                if (!wait(B_K_FULL + kb, (t >> 1) & 1)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DH / 16; ++k) {
+                    const uint64_t qd =
+                        umma_desc_k_sw128(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + (k / 4) * HQ * 128)) + 2 * (k % 4);
+                    const uint64_t kd =
+                        umma_desc_k_sw128(smem_u32(smem + C::OFF_K + kb * C::KV_TILE + (k / 4) * TK * 128)) + 2 * (k % 4);
+                    umma_bf16(tmem + hh * 128, qd, kd, idesc_s, k > 0);
+                }
+                umma_commit(bar(B_S_FULL + hh));
+                if (hh == tp.last_half(t)) umma_commit(bar(B_K_EMPTY + kb));
+                return true;
+            };
+            auto issue_pv = [&](int hh, int t) -> bool {
+                if (!wait(B_P_FULL + hh, t & 1)) return false;
+                if (hh == tp.first_half(t) && !wait(B_V_FULL, t & 1)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < TK / 16; ++k) {
+                    const uint64_t vd =
+                        umma_desc_k_sw128(smem_u32(smem + C::OFF_V + (k / 4) * DH * 128)) + 2 * (k % 4);
+                    umma_ts(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, vd, idesc_o, t > 0 || k > 0);
+                }
+                if (hh == tp.last_half(t)) umma_commit(bar(B_V_EMPTY));
+                if (t == tp.last[hh]) umma_commit(bar(B_O_FINAL + hh));
+                return true;
+            };
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+                if (ok && tp.active(hh, 0)) ok = issue_s(hh, 0);
+            for (int t = 0; t < tp.n_kt && ok; ++t) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (ok && tp.active(hh, t)) ok = issue_pv(hh, t);
+                    if (ok && tp.active(hh, t + 1)) ok = issue_s(hh, t + 1);
+                }
+            }
+            // nothing issued here may still run when tensor memory is released
+            umma_commit(bar(B_DRAIN));
+            (void)mbar_wait(bar(B_DRAIN), 0, limit);
+        }
+    } else if (warp >= kRebuildWarp0) {
+        // ---------------------------------------------------------------- K / V rebuild
+        const int rw = warp - kRebuildWarp0;
+        const int tok = lane >> 2;                 // slot of the 8-slot group this lane holds
+        const int blk = lane >> 3, brow = lane & 7;   // ldmatrix / stmatrix row this lane addresses
+        // One plane of local tile t: K (slot rows, stmatrix) or V^T (feature rows, stmatrix.trans).
+        auto rebuild = [&](int t, bool is_v) {
+            const int fs = t % C::FST;
+            const unsigned char *st = smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)fs * C::ST;
+            const uint32_t dst = smem_u32(smem + (is_v ? C::OFF_V : C::OFF_K + (t & 1) * C::KV_TILE));
+            const int t0 = tl.slot_tile(v0 + t) * TK;
+            const bool edge = !(t0 + TK - 1 <= hi && t0 >= wstart);
+#pragma unroll 1
+            for (int gi = 0; gi < TK / kGroup / kRebuildWarps; ++gi) {
+                const int g = rw * (TK / kGroup / kRebuildWarps) + gi;        // 8-slot group of the tile
+                const int lg = E4M3 ? g >> 1 : g, hf = g & 1;                 // its layout group, and half of it
+                // A_r[tok][j1]: one 16-byte row per j1 holds the group's slots
+                float av[R][8];
+                if constexpr (E4M3) {
+                    const unsigned char *e = st + C::FACT + lg * 32 + 2 * tok + hf;
+                    const float sc = exp_sum(((uint32_t)e[0] + e[16] + 130u) & 255u);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int j1 = 0; j1 < 8; ++j1)
+                            av[r][j1] = h2_to_f2(e4m3x2_to_h2(st[r * C::BOX + lg * 128 + j1 * 16 + 2 * tok + hf])).x * sc;
+                } else {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int j1 = 0; j1 < 8; ++j1)
+                            av[r][j1] = __uint_as_float(
+                                (uint32_t)(*reinterpret_cast<const uint16_t *>(st + r * C::BOX + lg * 128 + j1 * 16 + tok * 2))
+                                << 16);
+                }
+                // B_r[tok][hb*8 + 2c .. +1] for (r, hb) = block r * HB + hb
+                constexpr int NB = R * HB;
+                float2 bf[NB];
+                auto unpack = [&](uint32_t w) {
+                    if constexpr (E4M3) return h2_to_f2(e4m3x2_to_h2(__byte_perm(w, 0, hf ? 0x4431 : 0x4420)));
+                    return unpack_bf16x2(w);
+                };
+                if constexpr (HB == 2) {
+#pragma unroll
+                    for (int q4 = 0; q4 < NB / 4; ++q4) {          // four blocks (two ranks) per load
+                        uint32_t bw[4];
+                        ldsm_x4_t(smem_u32(st + (R + 4 * q4 + blk) * C::BOX + lg * 128 + brow * 16), bw);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) bf[4 * q4 + i] = unpack(bw[i]);
+                    }
+                } else {
+                    uint32_t bw[2];                                // lanes 0..15 address the two blocks
+                    ldsm_x2_t(smem_u32(st + (R + (blk & 1)) * C::BOX + lg * 128 + brow * 16), bw);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) bf[i] = unpack(bw[i]);
+                }
+                uint32_t w[8][HB];
+#pragma unroll
+                for (int j1 = 0; j1 < 8; ++j1)
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+                        float2 acc = fmul2(make_float2(av[0][j1], av[0][j1]), bf[hb]);
+#pragma unroll
+                        for (int r = 1; r < R; ++r)
+                            acc = ffma2(make_float2(av[r][j1], av[r][j1]), bf[r * HB + hb], acc);
+                        w[j1][hb] = pack_half2(acc.x, acc.y);
+                    }
+                if (edge && !seen(t0 + g * kGroup + tok)) {
+#pragma unroll
+                    for (int j1 = 0; j1 < 8; ++j1)
+#pragma unroll
+                        for (int hb = 0; hb < HB; ++hb) w[j1][hb] = 0u;
+                }
+                // this lane addresses row brow of block blk of each x4 store: d2 = 16, (j1 = 2i +
+                // blk/2, hb = blk%2); d2 = 8, j1 = 4i + blk
+#pragma unroll
+                for (int i = 0; i < 8 / (4 / HB); ++i) {
+                    const int f0 = HB == 2 ? (2 * i + (blk >> 1)) * 16 + (blk & 1) * 8 : (4 * i + blk) * 8;
+                    uint32_t w0, w1, w2, w3;
+                    if constexpr (HB == 2) {
+                        w0 = w[2 * i][0], w1 = w[2 * i][HB - 1], w2 = w[2 * i + 1][0], w3 = w[2 * i + 1][HB - 1];
+                    } else {
+                        w0 = w[4 * i][0], w1 = w[4 * i + 1][0], w2 = w[4 * i + 2][0], w3 = w[4 * i + 3][0];
+                    }
+                    if (!is_v) {
+                        const int row = g * kGroup + brow;                          // slot row
+                        const uint32_t ad = dst + (f0 >> 6) * (TK * 128) + sw128_chunk(row, (f0 & 63) >> 3);
+                        stsm_x4(ad, w0, w1, w2, w3);
+                    } else {
+                        const int row = f0 + brow;                                  // feature row
+                        const uint32_t ad = dst + (g >> 3) * (DH * 128) + sw128_chunk(row, g & 7);
+                        stsm_x4_t(ad, w0, w1, w2, w3);
+                    }
+                }
+            }
+        };
+        auto step = [&](int t, bool is_v) -> bool {
+            const int s = t & 1, fs = t % C::FST;           // K buffer, factor stage
+            bool ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (t / C::FST) & 1);
+            if (ok && !is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
+            if (ok && is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            rebuild(t, is_v);
+            fence_async_smem();        // visible to the tensor cores
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
+                mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
+            }
+            return true;
+        };
+        if (tp.n_kt > 0) {
+            bool ok = step(0, false);
+            for (int t = 0; t < tp.n_kt && ok; ++t) {
+                if (t + 1 < tp.n_kt) ok = step(t + 1, false);
+                if (ok) ok = step(t, true);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax rows
+        const int hh = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane, r = hh * HQ + row;
+        const bool exists = r < n;
+        const long long at = pos0 + r;
+        const bool live = exists && at >= 0 && at < a.p.max_len;
+        const size_t rh = (size_t)(row0 + r) * h + head;
+        if (tp.act[hh]) {
+            // Q_h: bf16 -> fp16 x qscale in place, once its copy has landed
+            bool ok = wait(B_Q, 0);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                uint4 *q4 = reinterpret_cast<uint4 *>(smem + C::OFF_Q + hh * C::Q_HALF);
+#pragma unroll 4
+                for (int i = row; i < (int)(C::Q_HALF / 16); i += HQ) {
+                    uint4 u = q4[i];
+                    uint32_t *wv = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = unpack_bf16x2(wv[k]);
+                        wv[k] = pack_half2(x.x * a.p.qscale, x.y * a.p.qscale);
+                    }
+                    q4[i] = u;
+                }
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_QREADY + hh));
+
+            const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+            const uint32_t s_addr = tmem + lane_off + hh * 128;
+            const uint32_t o_addr = tmem + lane_off + 256 + hh * 128;
+            const int pos = live ? (int)at : -1;                         // (-1 sees nothing)
+            const int wlow = window_start(a.p.mask, pos);
+            const int half_lo = (int)max(pos0 + hh * HQ, 0ll);           // smallest position of the half
+            const int half_w = window_start(a.p.mask, (int)min(pos0 + min(n, (hh + 1) * HQ) - 1, (long long)hi));
+            const bool all_live = pos0 + hh * HQ >= 0 && pos0 + min(n, (hh + 1) * HQ) <= a.p.max_len;
+            float m_used = -INFINITY, l_run = 0.f;
+            for (int t = 0; t <= tp.last[hh] && ok; ++t) {
+                ok = __all_sync(0xffffffffu, wait(B_S_FULL + hh, t & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int t0 = tl.slot_tile(v0 + t) * TK;
+                const bool masked = t0 + TK - 1 > half_lo || t0 < half_w || !all_live;
+                // slots j <= lim of the tile, from low on or below sink, are visible
+                const int lim = pos - t0, low = wlow - t0, sink = a.p.mask.sinks - t0;
+                auto hidden = [&](int j) { return j > lim || (j < low && j >= sink); };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < TK / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(s_addr + c * 32, v);
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (hidden(c * 32 + j)) v[j] = -INFINITY;
+                    }
+                    float ma = fmax3(mx, v[0], v[1]), mb = fmax3(v[2], v[3], v[4]);
+#pragma unroll
+                    for (int j = 5; j < 29; j += 4) {
+                        ma = fmax3(ma, v[j], v[j + 1]);
+                        mb = fmax3(mb, v[j + 2], v[j + 3]);
+                    }
+                    mx = fmax3(ma, mb, fmax3(v[29], v[30], v[31]));
+                }
+                const bool grow = mx > m_used + kRescaleLog2;
+                float alpha = 1.f;
+                if (grow) {
+                    alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mx);
+                    m_used = mx;
+                    l_run *= alpha;
+                }
+                if (t > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                    for (int c = 0; c < DH / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(o_addr + c * 32, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= alpha;
+                        tmem_st32(o_addr + c * 32, v);
+                    }
+                }
+                const float mref = m_used == -INFINITY ? 0.f : m_used;
+                const float2 mref2 = make_float2(mref, mref);
+                float2 suma = make_float2(0.f, 0.f), sumb = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < TK / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(s_addr + c * 32, v);
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int jp = 0; jp < 16; ++jp) {
+                        const float2 x = fsub2(make_float2(v[2 * jp], v[2 * jp + 1]), mref2);
+                        // one pair in four on the FMA pipe, the rest on the transcendental unit
+                        float2 p = (jp & 3) == 3 ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
+                        if (masked) {
+                            if (hidden(c * 32 + 2 * jp)) p.x = 0.f;
+                            if (hidden(c * 32 + 2 * jp + 1)) p.y = 0.f;
+                        }
+                        if (jp & 1)
+                            sumb = fadd2(sumb, p);
+                        else
+                            suma = fadd2(suma, p);
+                        pw[jp] = pack_half2(p.x, p.y);
+                    }
+                    tmem_st16u(s_addr + c * 16, pw);                  // P over the S columns already read
+                }
+                l_run += (suma.x + suma.y) + (sumb.x + sumb.y);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P_FULL + hh));
+            }
+            // epilogue: one row per thread, normalised or as this split's partial
+            if (ok) ok = __all_sync(0xffffffffu, wait(B_O_FINAL + hh, 0));
+            if (ok) {
+                tc_fence_after();
+                bool finite = true;
+                const bool whole = a.p.n_split == 1;
+                const float inv = !whole ? 1.f : (l_run == 0.f ? 0.f : a.p.out_scale / l_run);
+                if (!whole && exists) {
+                    *reinterpret_cast<float2 *>(a.p.part_ml + (rh * a.p.n_split + split) * 2) =
+                        make_float2(live ? m_used : -INFINITY, live ? l_run : 0.f);
+                    finite = !live || (l_run <= 3.4e38f && m_used <= 3.4e38f);
+                }
+#pragma unroll 1
+                for (int c = 0; c < DH / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(o_addr + c * 32, v);
+                    if (exists) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * inv : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) finite &= fabsf(v[j]) <= 3.4e38f;
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                __nv_bfloat162 o2[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) o2[k] = __floats2bfloat162_rn(v[j + 2 * k], v[j + 2 * k + 1]);
+                                *reinterpret_cast<uint4 *>(a.p.out + rh * DH + c * 32 + j) = *reinterpret_cast<const uint4 *>(o2);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<float4 *>(a.p.part_o + (rh * a.p.n_split + split) * DH + c * 32 + j) =
+                                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        }
+                    }
+                }
+                if (!finite) raise_error(a.p.err, kErrDeviceCheck);
+            }
+        } else if (exists) {                                          // no tile of this half here
+            if (a.p.n_split > 1) {
+                *reinterpret_cast<float2 *>(a.p.part_ml + (rh * a.p.n_split + split) * 2) = make_float2(-INFINITY, 0.f);
+            } else {
+                for (int c = 0; c < DH; c += 8)
+                    *reinterpret_cast<uint4 *>(a.p.out + rh * DH + c) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// A pool plane viewed as [groups][E rows] of 16 bytes (32-bit elements): boxes of 8 rows x
+// `rows` groups, no swizzle.
+bool make_plane_map(CUtensorMap *map, const void *plane, uint64_t groups, uint64_t group_bytes, int rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {group_bytes / 4, groups};
+    cuuint64_t strides[1] = {group_bytes};
+    cuuint32_t box[2] = {32, (cuuint32_t)rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void *>(plane), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned long long wait_limit_ns, cudaStream_t st) {
+    PrefillArgsP a;
+    a.p = p;
+    a.pool = s.pool;
+    a.h1 = s.d.h1;
+    a.h2 = s.d.h2;
+    a.wait_limit_ns = wait_limit_ns;
+    a.box_groups = 8;                            // as many groups as every aligned run of them shares a page
+    while (s.pool.pg % a.box_groups != 0) a.box_groups /= 2;
+    CUtensorMap tmq, tmk, tmv;
+    const uint64_t sub = C::E4M3 ? 1 : 2, groups = (uint64_t)s.pool.n_pages * s.pool.pg * sub;
+    const int rows = a.box_groups * (int)sub;
+    if (!make_q_map(&tmq, p.q, (uint64_t)p.n_rows, (uint64_t)s.d.h * s.d.dh, HQ) ||
+        !make_plane_map(&tmk, s.pool.k, groups, (uint64_t)s.pool.kg / sub, rows) ||
+        !make_plane_map(&tmv, s.pool.v, groups, (uint64_t)s.pool.vg / sub, rows))
+        return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dynamic_smem<paged_prefill_kernel<C>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = (unsigned)(((long long)p.n_rows + (long long)p.batch * (2 * HQ - 1)) / (2 * HQ));
+    paged_prefill_kernel<C><<<dim3(tiles, (unsigned)s.d.h, (unsigned)p.n_split), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.n_split == 1) return e;
+    return launch_paged_combine(s, p, st);
+}
+
+}  // namespace
+
+int paged_prefill_rows() { return 2 * HQ; }
+
+bool paged_prefill_supported(const PagedShape &s) {
+    const Dims &d = s.d;
+    // group coordinates of the tensor maps are 32-bit
+    if ((uint64_t)s.pool.n_pages * s.pool.pg * 2 > INT32_MAX) return false;
+    return d.d1 == 8 && d.rk == d.rv && ((d.d2 == 16 && (d.rk == 2 || d.rk == 4)) || (d.d2 == 8 && d.rk == 2));
+}
+
+cudaError_t launch_paged_prefill(const PagedShape &s, const PagedAttnArgs &a, unsigned long long wait_limit_ns,
+                                 cudaStream_t st) {
+    if (!paged_prefill_supported(s)) return cudaErrorInvalidValue;
+    const bool q8 = s.pool.e4m3 != 0;
+    if (s.d.d2 == 8)
+        return q8 ? launch_cfg<Cfg<8, 2, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<8, 2, false>>(s, a, wait_limit_ns, st);
+    if (s.d.rk == 4)
+        return q8 ? launch_cfg<Cfg<16, 4, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<16, 4, false>>(s, a, wait_limit_ns, st);
+    return q8 ? launch_cfg<Cfg<16, 2, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<16, 2, false>>(s, a, wait_limit_ns, st);
+}
+
+}  // namespace kpa
