@@ -56,30 +56,37 @@ __device__ __forceinline__ Tiles visible_tiles(const Mask &m, int lo, int hi, in
     return t;
 }
 
-// Rows of one sequence: checked against [0, n_rows]; false (no rows) where they are not.
-__device__ __forceinline__ bool rows_of(const int32_t *cu, int b, int n_rows, int &r0, int &r1) {
-    r0 = cu[b];
-    r1 = cu[b + 1];
-    return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
-}
-
-// Finds the sequence that unit `idx` falls to when sequence b has count(b, bad) units, laid
-// one sequence after the other.  Every thread of the block calls it; returns the sequence
-// (or -1 past the last unit) and the unit's index inside it.  THREADS threads, a scan of
-// THREADS sequences per step, to the end of the batch for the block that reports bad ones.
+// Finds the sequence that unit `idx` falls to when a sequence of n rows from position p has
+// count(p, n) units, laid one sequence after the other: its rows r0 .. r0 + n - 1, its first
+// position and the unit's index i inside it (b = -1 past the last unit).  Every thread of the
+// block calls it; THREADS threads, a scan of THREADS sequences per step, to the end of the
+// batch for the block that reports sequences with rows outside [0, n_rows].
 struct Found {
-    int b, i;
+    int b, i, r0, n, pos;
 };
 template <int THREADS, class Count>
-__device__ __forceinline__ Found find_unit(int idx, int batch, bool to_end, Count count) {
+__device__ __forceinline__ Found find_unit(int idx, const int32_t *cu, const int32_t *start, int batch, int n_rows,
+                                           int *err, Count count) {
     __shared__ int warp_sum[THREADS / 32];
-    __shared__ int hit_b, hit_i;
+    __shared__ Found hit;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) hit_b = -1;
+    if (tid == 0) hit.b = -1;
     int before = 0;
     for (int base = 0; base < batch; base += THREADS) {
         const int b = base + tid;
-        const int c = b < batch ? count(b) : 0;
+        int c = 0;
+        Found f = {b, 0, 0, 0, 0};
+        if (b < batch) {
+            f.r0 = cu[b];
+            const int r1 = cu[b + 1];
+            f.pos = start[b];
+            if (f.r0 < 0 || r1 < f.r0 || r1 > n_rows) {
+                if (idx == 0) raise_error(err, kErrDeviceCheck);
+            } else {
+                f.n = r1 - f.r0;
+                c = f.n > 0 ? count(f.pos, f.n) : 0;
+            }
+        }
         int inc = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -97,18 +104,14 @@ __device__ __forceinline__ Found find_unit(int idx, int batch, bool to_end, Coun
         }
         const int lo = pre + inc - c;
         if (idx >= lo && idx < lo + c) {
-            hit_b = b;
-            hit_i = idx - lo;
+            f.i = idx - lo;
+            hit = f;
         }
         __syncthreads();
         before = total;
-        if (idx < before && !to_end) break;
+        if (idx != 0 && idx < before) break;
     }
-    Found f;
-    f.b = hit_b;
-    f.i = hit_i;
-    __syncthreads();
-    return f;
+    return hit;
 }
 
 // ---- e4m3

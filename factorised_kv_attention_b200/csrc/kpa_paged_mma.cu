@@ -128,19 +128,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const MmaArgs a)
     int b, row0, n;
     long long pos0;
     if (a.p.cu) {
-        const Found f = find_unit<kThreads>(blockIdx.x, a.p.batch, blockIdx.x == 0, [&](int s) {
-            int r0, r1;
-            if (!rows_of(a.p.cu, s, a.p.n_rows, r0, r1)) {
-                if (blockIdx.x == 0) raise_error(a.p.err, kErrDeviceCheck);
-                return 0;
-            }
-            return (r1 - r0 + kRows - 1) / kRows;
-        });
+        const Found f = find_unit<kThreads>(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
+                                            [](int, int rows) { return (rows + kRows - 1) / kRows; });
         if (f.b < 0) return;
         b = f.b;
-        row0 = a.p.cu[b] + f.i * kRows;
-        n = min(kRows, a.p.cu[b + 1] - row0);
-        pos0 = (long long)a.p.start[b] + f.i * kRows;
+        row0 = f.r0 + f.i * kRows;
+        n = min(kRows, f.n - f.i * kRows);
+        pos0 = (long long)f.pos + f.i * kRows;
     } else {
         b = row0 = blockIdx.x;
         n = 1;

@@ -125,19 +125,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
 
     // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r; the last rows of a
     // sequence, which see most, first
-    const Found f = find_unit<kThreads>(blockIdx.x, a.p.batch, blockIdx.x == 0, [&](int s) {
-        int r0, r1;
-        if (!rows_of(a.p.cu, s, a.p.n_rows, r0, r1)) {
-            if (blockIdx.x == 0) raise_error(a.p.err, kErrDeviceCheck);
-            return 0;
-        }
-        return (r1 - r0 + 2 * HQ - 1) / (2 * HQ);
-    });
+    const Found f = find_unit<kThreads>(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
+                                        [](int, int rows) { return (rows + 2 * HQ - 1) / (2 * HQ); });
     if (f.b < 0) return;
-    const int b = f.b, seq0 = a.p.cu[b], seq_n = a.p.cu[b + 1] - seq0;
-    const int q0 = ((seq_n + 2 * HQ - 1) / (2 * HQ) - 1 - f.i) * 2 * HQ;
-    const int row0 = seq0 + q0, n = min(2 * HQ, seq_n - q0);
-    const long long pos0 = (long long)a.p.start[b] + q0;
+    const int b = f.b, q0 = ((f.n + 2 * HQ - 1) / (2 * HQ) - 1 - f.i) * 2 * HQ;
+    const int row0 = f.r0 + q0, n = min(2 * HQ, f.n - q0);
+    const long long pos0 = (long long)f.pos + q0;
     if (tid == 0 && (pos0 < 0 || pos0 + n > a.p.max_len)) raise_error(a.p.err, kErrDeviceCheck);
 
     // ---- tiles: what the rows with a position in [0, max_len) see
@@ -504,16 +497,21 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 const bool masked = t0 + TK - 1 > half_lo || t0 < half_w || !all_live;
                 // slots j <= lim of the tile, from low on or below sink, are visible
                 const int lim = pos - t0, low = wlow - t0, sink = a.p.mask.sinks - t0;
-                auto hidden = [&](int j) { return j > lim || (j < low && j >= sink); };
+                // the visible ones of slots 32 c .. 32 c + 31 as bits
+                auto upto = [](int j) { return j < 0 ? 0u : j >= 31 ? 0xffffffffu : (2u << j) - 1u; };   // bits 0 .. j
+                auto visible = [&](int c) {
+                    return upto(lim - c * 32) & (~upto(low - 1 - c * 32) | upto(sink - 1 - c * 32));
+                };
                 float mx = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < TK / 32; ++c) {
                     float v[32];
                     tmem_ld32(s_addr + c * 32, v);
                     if (masked) {
+                        const uint32_t vis = visible(c);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (hidden(c * 32 + j)) v[j] = -INFINITY;
+                            if (!(vis >> j & 1u)) v[j] = -INFINITY;
                     }
                     float ma = fmax3(mx, v[0], v[1]), mb = fmax3(v[2], v[3], v[4]);
 #pragma unroll
@@ -548,14 +546,15 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     float v[32];
                     tmem_ld32(s_addr + c * 32, v);
                     uint32_t pw[16];
+                    const uint32_t vis = masked ? visible(c) : 0xffffffffu;
 #pragma unroll
                     for (int jp = 0; jp < 16; ++jp) {
                         const float2 x = fsub2(make_float2(v[2 * jp], v[2 * jp + 1]), mref2);
                         // one pair in four on the FMA pipe, the rest on the transcendental unit
                         float2 p = (jp & 3) == 3 ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
                         if (masked) {
-                            if (hidden(c * 32 + 2 * jp)) p.x = 0.f;
-                            if (hidden(c * 32 + 2 * jp + 1)) p.y = 0.f;
+                            if (!(vis >> (2 * jp) & 1u)) p.x = 0.f;
+                            if (!(vis >> (2 * jp + 1) & 1u)) p.y = 0.f;
                         }
                         if (jp & 1)
                             sumb = fadd2(sumb, p);

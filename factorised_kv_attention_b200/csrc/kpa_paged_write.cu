@@ -34,16 +34,6 @@ struct WriteArgs {
 
 // 16-slot groups that the rows of sequence b touch.
 __device__ __forceinline__ long long floor16(long long a) { return a >= 0 ? a / 16 : -((-a + 15) / 16); }
-__device__ __forceinline__ int groups_of(const WriteArgs &a, int b) {
-    int r0, r1;
-    if (!rows_of(a.cu, b, a.n_rows, r0, r1)) {
-        if (blockIdx.x == 0) raise_error(a.err, kErrDeviceCheck);
-        return 0;
-    }
-    if (r1 == r0) return 0;
-    const long long s0 = a.start[b];
-    return (int)(floor16(s0 + (r1 - r0) - 1) - floor16(s0)) + 1;
-}
 
 // byte of slot t inside a row of an e4m3 group
 __device__ __forceinline__ int byte_of(int t) { return 2 * (t & 7) + (t >> 3); }
@@ -59,14 +49,16 @@ struct Group {
 // The group of this CTA: false when there is none.
 template <class Plane>
 __device__ __forceinline__ bool my_group(const WriteArgs &a, Plane *plane, int bytes, Group &g) {
-    const Found f = find_unit<kThreads>(blockIdx.x, a.batch, blockIdx.x == 0, [&](int b) { return groups_of(a, b); });
+    const Found f = find_unit<kThreads>(blockIdx.x, a.cu, a.start, a.batch, a.n_rows, a.err, [](long long s, int n) {
+        return (int)(floor16(s + n - 1) - floor16(s)) + 1;
+    });
     if (f.b < 0) return false;
-    const long long s0 = a.start[f.b], n = a.cu[f.b + 1] - a.cu[f.b];
+    const long long s0 = f.pos, n = f.n;
     const long long gi = floor16(s0) + f.i;
     g.slot0 = gi * 16;
     g.t0 = (int)max(0ll, s0 - g.slot0);
     g.t1 = (int)min(16ll, s0 + n - g.slot0);
-    g.row0 = a.cu[f.b] + (int)(g.slot0 + g.t0 - s0);
+    g.row0 = f.r0 + (int)(g.slot0 + g.t0 - s0);
     g.dst = nullptr;
     bool ok = g.slot0 >= 0 && g.slot0 + 16 <= a.max_slots;      // (the range is whole groups)
     if (ok) {
