@@ -59,20 +59,21 @@ __device__ __forceinline__ Tiles visible_tiles(const Mask &m, int lo, int hi, in
 // Finds the sequence that unit `idx` falls to when a sequence of n rows from position p has
 // count(p, n) units, laid one sequence after the other: its rows r0 .. r0 + n - 1, its first
 // position and the unit's index i inside it (b = -1 past the last unit).  Every thread of the
-// block calls it; THREADS threads, a scan of THREADS sequences per step, to the end of the
-// batch for the block that reports sequences with rows outside [0, n_rows].
+// block calls it (whole warps, at most 32); each step scans as many sequences as the block has
+// threads, to the end of the batch in the block that reports sequences with rows outside
+// [0, n_rows].
 struct Found {
     int b, i, r0, n, pos;
 };
-template <int THREADS, class Count>
+template <class Count>
 __device__ __forceinline__ Found find_unit(int idx, const int32_t *cu, const int32_t *start, int batch, int n_rows,
                                            int *err, Count count) {
-    __shared__ int warp_sum[THREADS / 32];
+    __shared__ int warp_sum[32];
     __shared__ Found hit;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     if (tid == 0) hit.b = -1;
     int before = 0;
-    for (int base = 0; base < batch; base += THREADS) {
+    for (int base = 0; base < batch; base += threads) {
         const int b = base + tid;
         int c = 0;
         Found f = {b, 0, 0, 0, 0};
@@ -96,8 +97,7 @@ __device__ __forceinline__ Found find_unit(int idx, const int32_t *cu, const int
         if (lane == 31) warp_sum[warp] = inc;
         __syncthreads();
         int pre = before, total = before;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
+        for (int w = 0; w < threads / 32; ++w) {
             const int s = warp_sum[w];
             if (w < warp) pre += s;
             total += s;

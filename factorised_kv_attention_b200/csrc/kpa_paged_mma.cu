@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const MmaArgs a)
     int b, row0, n;
     long long pos0;
     if (a.p.cu) {
-        const Found f = find_unit<kThreads>(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
+        const Found f = find_unit(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
                                             [](int, int rows) { return (rows + kRows - 1) / kRows; });
         if (f.b < 0) return;
         b = f.b;

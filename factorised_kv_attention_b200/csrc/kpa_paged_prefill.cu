@@ -125,7 +125,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
 
     // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r; the last rows of a
     // sequence, which see most, first
-    const Found f = find_unit<kThreads>(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
+    const Found f = find_unit(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
                                         [](int, int rows) { return (rows + 2 * HQ - 1) / (2 * HQ); });
     if (f.b < 0) return;
     const int b = f.b, q0 = ((f.n + 2 * HQ - 1) / (2 * HQ) - 1 - f.i) * 2 * HQ;

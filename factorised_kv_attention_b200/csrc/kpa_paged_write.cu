@@ -6,10 +6,16 @@
 // the scales of a Kronecker product's two factors multiply into one number per token.
 //
 // Both directions transpose between token-major records and the pages' element-major
-// groups.  One CTA takes one 16-slot group of one plane: the records are read and written
-// in order (one warp per token), the group's rows as 16-byte vectors, and the transposition
-// goes through shared memory in pieces of kPiece elements, so any record length fits.
-// Bound by memory: nothing is read or written twice.
+// groups.  One CTA takes one 16-slot group of one plane, one thread two neighbouring elements
+// of all 16 slots: a warp reads (writes) 128 contiguous bytes of each record and writes
+// (reads) whole 16-byte rows of the group, and the transposition is the thread's registers.
+// Nothing goes through shared memory but the rotation table and the largest magnitudes of
+// the 16 tokens.  Bound by latency at a few tokens and by memory beyond.
+#include <string.h>
+
+#include <algorithm>
+#include <type_traits>
+
 #include "kpa_paged.cuh"
 
 namespace kpa {
@@ -17,8 +23,8 @@ namespace {
 
 using namespace paged;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPiece = 512;                       // elements of a record staged at a time
+
+constexpr int kMaxThreads = 512;
 
 struct WriteArgs {
     Pool pool;
@@ -39,44 +45,38 @@ __device__ __forceinline__ long long floor16(long long a) { return a >= 0 ? a / 
 __device__ __forceinline__ int byte_of(int t) { return 2 * (t & 7) + (t >> 3); }
 
 struct Group {
+    int b;                                        // its sequence
     int row0;                                     // row of the group's first token here
     int t0, t1;                                   // its tokens: slots t0 .. t1 - 1 of the group
     long long slot0;                              // first slot of the group
-    unsigned char *dst;                           // the group in the pool plane, or null
-    bool any;
 };
 
 // The group of this CTA: false when there is none.
-template <class Plane>
-__device__ __forceinline__ bool my_group(const WriteArgs &a, Plane *plane, int bytes, Group &g) {
-    const Found f = find_unit<kThreads>(blockIdx.x, a.cu, a.start, a.batch, a.n_rows, a.err, [](long long s, int n) {
+__device__ __forceinline__ bool find_group(const WriteArgs &a, Group &g) {
+    const Found f = find_unit(blockIdx.x, a.cu, a.start, a.batch, a.n_rows, a.err, [](long long s, int n) {
         return (int)(floor16(s + n - 1) - floor16(s)) + 1;
     });
     if (f.b < 0) return false;
     const long long s0 = f.pos, n = f.n;
-    const long long gi = floor16(s0) + f.i;
-    g.slot0 = gi * 16;
+    g.b = f.b;
+    g.slot0 = (floor16(s0) + f.i) * 16;
     g.t0 = (int)max(0ll, s0 - g.slot0);
     g.t1 = (int)min(16ll, s0 + n - g.slot0);
     g.row0 = f.r0 + (int)(g.slot0 + g.t0 - s0);
-    g.dst = nullptr;
-    bool ok = g.slot0 >= 0 && g.slot0 + 16 <= a.max_slots;      // (the range is whole groups)
-    if (ok) {
-        int entry, in;
-        split_group(a.pool, (int)gi, entry, in);
-        const int page = a.pool.table[(size_t)f.b * a.pool.table_stride + entry];
-        ok = page >= 0 && page < a.pool.n_pages;
-        if (ok) g.dst = (unsigned char *)plane + ((size_t)page * a.pool.pg + in) * (size_t)bytes;
-    }
-    if (!ok && threadIdx.x == 0) raise_error(a.err, kErrDeviceCheck);
     return true;
 }
 
-// Two neighbouring elements e, e + 1 of a record (e even when VEC: one 4-byte load).
-template <bool VEC>
-__device__ __forceinline__ float2 load2(const __nv_bfloat16 *r, int e) {
-    if constexpr (VEC) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(r + e));
-    return make_float2(__bfloat162float(r[e]), __bfloat162float(r[e + 1]));
+// Where it lies in a pool plane, or null: reported.
+template <class Byte>
+__device__ __forceinline__ Byte *group_at(const WriteArgs &a, const Group &g, Byte *plane, int bytes) {
+    if (g.slot0 >= 0 && g.slot0 + 16 <= a.max_slots) {          // (the table's range is whole groups)
+        int entry, in;
+        split_group(a.pool, (int)(g.slot0 >> 4), entry, in);
+        const int page = __ldg(a.pool.table + (size_t)g.b * a.pool.table_stride + entry);
+        if (page >= 0 && page < a.pool.n_pages) return plane + ((size_t)page * a.pool.pg + in) * (size_t)bytes;
+    }
+    if (threadIdx.x == 0) raise_error(a.err, kErrDeviceCheck);
+    return nullptr;
 }
 
 __device__ __forceinline__ float finite_abs(float x) {
@@ -92,181 +92,233 @@ __device__ __forceinline__ int scale_byte(float m) {
     return min(max(e, 63), 190);
 }
 
+// Largest of each of 16 values over the warp: lane l returns that of value
+// 8 l[4] + 4 l[3] + 2 l[2] + l[1] (bits of l).  Each step trades half of the values.
+__device__ __forceinline__ float warp_max16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int n = 8; n >= 1; n >>= 1) {
+        const bool up = lane & (2 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+            v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 2 * n));
+        }
+    }
+    return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+// VEC: records, and their B parts, start on 4-byte boundaries (two elements per load).
 template <bool E4M3, bool VEC>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(WriteArgs a, RopeTable rope) {
-    // e4m3: [kPiece][16] codes; bf16: [2][kPiece][8]
-    __shared__ __align__(16) unsigned char tile[kPiece * (E4M3 ? 16 : 32)];
-    __shared__ float2 cs[16][kMaxHalfD2 + 1];
-    __shared__ uint32_t scales[16];               // exponent bytes: A in the low byte, B in the next
+__global__ void __launch_bounds__(kMaxThreads, 2) paged_append_kernel(WriteArgs a, RopeTable rope) {
+    extern __shared__ float2 cs[];                // [d2 / 2][16]: (cos, sin) of pair m at slot t
+    __shared__ unsigned top[2][16];               // bits of the parts' largest magnitudes
     const bool is_k = blockIdx.y == 0;
     const int E = is_k ? a.ek : a.ev, A = is_k ? a.ak : a.av;
+    const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+    if (tid < 32) top[tid >> 4][tid & 15] = 0u;   // (the scan below synchronises)
     Group g;
-    if (!my_group(a, is_k ? a.kpool : a.vpool, is_k ? a.pool.kg : a.pool.vg, g) || !g.dst) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!find_group(a, g)) return;
     const int half = a.d2 / 2;
+    // Pair p is elements 2p, 2p + 1 of A, then of B; the last pair of an odd A has one.
+    const int pa = (A + 1) / 2, pairs = pa + (E - A) / 2;
+    const __nv_bfloat16 *src = (is_k ? a.kf : a.vf) + (size_t)g.row0 * E - (size_t)g.t0 * E;
+    uint32_t x[16];
+    auto load = [&](int p) {
+        const int e = p >= pa ? A + 2 * (p - pa) : 2 * p;
+        const bool one = p < pa && e + 1 >= A;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            x[t] = 0u;
+            if (p < pairs && t >= g.t0 && t < g.t1) {
+                const __nv_bfloat16 *r = src + (size_t)t * E + e;
+                if (VEC)
+                    x[t] = __ldg(reinterpret_cast<const uint32_t *>(r));
+                else
+                    x[t] = (uint32_t)__bfloat16_as_ushort(r[0]) | (one ? 0u : (uint32_t)__bfloat16_as_ushort(r[1]) << 16);
+            }
+        }
+    };
+    float2 v[16];                                 // the pair's values, rotated for a key's B
+    auto rotate = [&](int p) {
+        const bool turn = is_k && p >= pa && p < pairs;
+        const float2 *w = cs + (turn ? ((p - pa) % half) * 16 : 0);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            v[t] = make_float2(__uint_as_float(x[t] << 16), __uint_as_float(x[t] & 0xffff0000u));
+            if (turn) v[t] = make_float2(v[t].x * w[t].x - v[t].y * w[t].y, v[t].x * w[t].y + v[t].y * w[t].x);
+        }
+    };
+    load(tid);                                    // in flight while the table entry and the angles are
+    unsigned char *const dst0 = group_at(a, g, is_k ? a.kpool : a.vpool, is_k ? a.pool.kg : a.pool.vg);
+    if (!dst0) return;
     if (is_k) {
-        for (int i = tid; i < (g.t1 - g.t0) * half; i += kThreads) {
-            const int t = g.t0 + i / half, m = i % half;
-            float c, s;
-            rope_cs((double)(g.slot0 + t), rope.theta[m], c, s);
-            cs[t][m] = make_float2(c, s);
+        for (int i = tid; i < 16 * half; i += threads) {
+            const int t = i & 15;
+            float c = 0.f, s = 0.f;               // (the rotation of an absent slot's zeros)
+            if (t >= g.t0 && t < g.t1) rope_cs((double)(g.slot0 + t), rope.theta[i >> 4], c, s);
+            cs[i] = make_float2(c, s);
         }
         __syncthreads();
     }
-    const __nv_bfloat16 *src = is_k ? a.kf : a.vf;
-    // Elements 2p, 2p + 1 counted over A then B, each part rounded up to whole pairs; the
-    // second element of an odd A part's last pair is absent (dropped by every user).
-    const int pa = (A + 1) / 2, pairs = pa + (E - A) / 2;
-    auto pair_at = [&](const __nv_bfloat16 *r, int t, int p, int &e, bool &one) -> float2 {
-        const bool in_b = p >= pa;
-        e = in_b ? A + 2 * (p - pa) : 2 * p;
-        one = !in_b && e + 1 >= A;
-        if (one) return make_float2(__bfloat162float(r[e]), 0.f);
-        float2 x = load2<VEC>(r, e);
-        if (in_b && is_k) {
-            const float2 w = cs[t][(p - pa) % half];
-            x = make_float2(x.x * w.x - x.y * w.y, x.x * w.y + x.y * w.x);
-        }
-        return x;
-    };
+    rotate(tid);
+    const bool once = pairs <= threads;           // the values stay in registers
     if constexpr (E4M3) {
-        for (int t = g.t0 + warp; t < g.t1; t += kWarps) {
-            const __nv_bfloat16 *r = src + (size_t)(g.row0 + t - g.t0) * E;
-            float ma = 0.f, mb = 0.f;
-            for (int p = lane; p < pairs; p += 32) {
-                int e;
-                bool one;
-                const float2 x = pair_at(r, t, p, e, one);
-                const float m = fmaxf(finite_abs(x.x), finite_abs(x.y));
-                if (p >= pa)
-                    mb = fmaxf(mb, m);
-                else
-                    ma = fmaxf(ma, m);
+        const int token = ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+        for (int p0 = 0; p0 < pairs; p0 += threads) {
+            const int p = p0 + tid;
+            if (p0) {
+                load(p);
+                rotate(p);
             }
+            const bool in_b = p >= pa;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+                if (!__any_sync(0xffffffffu, in_b == (part == 1))) continue;
+                float w[16];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, off));
-                mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+                for (int t = 0; t < 16; ++t) w[t] = in_b == (part == 1) ? fmaxf(finite_abs(v[t].x), finite_abs(v[t].y)) : 0.f;
+                const float mx = warp_max16(w, lane);
+                if (!(lane & 1)) atomicMax(&top[part][token], __float_as_uint(mx));   // magnitudes: ordered as bits
             }
-            if (lane == 0) scales[t] = (uint32_t)scale_byte(ma) | ((uint32_t)scale_byte(mb) << 8);
         }
         __syncthreads();
-        // the scale rows
-        if (tid >= g.t0 && tid < g.t1) {
-            g.dst[(size_t)E * 16 + byte_of(tid)] = (unsigned char)(scales[tid] & 255u);
-            g.dst[(size_t)(E + 1) * 16 + byte_of(tid)] = (unsigned char)(scales[tid] >> 8);
+        if (tid < 32) {                           // the two scale rows
+            const int part = tid >> 4, t = tid & 15;
+            if (t >= g.t0 && t < g.t1)
+                dst0[(size_t)(E + part) * 16 + byte_of(t)] = (unsigned char)scale_byte(__uint_as_float(top[part][t]));
         }
     }
     const bool full = g.t0 == 0 && g.t1 == 16;
-    for (int p0 = 0; p0 < pairs; p0 += kPiece / 2) {
-        const int p1 = min(p0 + kPiece / 2, pairs);
-        // elements [e0, e1) of this piece
-        auto elem = [&](int p) { return p >= pa ? A + 2 * (p - pa) : 2 * p; };
-        const int e0 = elem(p0), e1 = p1 == pairs ? E : elem(p1);
-        if (p0) __syncthreads();
-        for (int t = g.t0 + warp; t < g.t1; t += kWarps) {
-            const __nv_bfloat16 *r = src + (size_t)(g.row0 + t - g.t0) * E;
-            float sa = 1.f, sb = 1.f;
-            if constexpr (E4M3) {                 // 2^-e, e = byte - 127 in [-64, 63]
-                sa = exp_byte(254u - (scales[t] & 255u));
-                sb = exp_byte(254u - (scales[t] >> 8));
-            }
-            for (int p = p0 + lane; p < p1; p += 32) {
-                int e;
-                bool one;
-                float2 x = pair_at(r, t, p, e, one);
-                if constexpr (E4M3) {
-                    const float s = p >= pa ? sb : sa;
-                    // infinities become NaN (the conversion would saturate them)
-                    x.x = fabsf(x.x) <= 3.4028235e38f ? x.x * s : __uint_as_float(0x7fffffffu);
-                    x.y = fabsf(x.y) <= 3.4028235e38f ? x.y * s : __uint_as_float(0x7fffffffu);
-                    const uint32_t c = to_e4m3x2(x.x, x.y);
-                    tile[(e - e0) * 16 + byte_of(t)] = (unsigned char)(c & 255u);
-                    if (!one) tile[(e + 1 - e0) * 16 + byte_of(t)] = (unsigned char)(c >> 8);
-                } else {
-                    __nv_bfloat16 *tb = reinterpret_cast<__nv_bfloat16 *>(tile) + (t >> 3) * (kPiece * 8);
-                    tb[(e - e0) * 8 + (t & 7)] = __float2bfloat16_rn(x.x);
-                    if (!one) tb[(e + 1 - e0) * 8 + (t & 7)] = __float2bfloat16_rn(x.y);
-                }
-            }
+    for (int p0 = 0; p0 < pairs; p0 += threads) {
+        const int p = p0 + tid;
+        if (!once) {
+            load(p);
+            rotate(p);
         }
-        __syncthreads();
-        const int n = e1 - e0;
+        if (p >= pairs) break;
+        const int e = p >= pa ? A + 2 * (p - pa) : 2 * p;
+        const bool one = p < pa && e + 1 >= A;
         if constexpr (E4M3) {
-            unsigned char *dst = g.dst + (size_t)e0 * 16;
-            if (full) {
-                for (int i = tid; i < n; i += kThreads)
-                    reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(tile)[i];
-            } else {
-                const int nt = g.t1 - g.t0;
-                for (int i = tid; i < n * nt; i += kThreads) {
-                    const int e = i / nt, o = e * 16 + byte_of(g.t0 + i % nt);
-                    dst[o] = tile[o];
+            uint32_t w0[4] = {0, 0, 0, 0}, w1[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {         // slots k and k + 8: neighbouring bytes
+                float2 y[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = k + 8 * u;
+                    // 2^-e, e = byte - 127 in [-64, 63]
+                    const float s = exp_byte(254u - (uint32_t)scale_byte(__uint_as_float(top[p >= pa][t])));
+                    // infinities become NaN (the conversion would saturate them)
+                    y[u].x = fabsf(v[t].x) <= 3.4028235e38f ? v[t].x * s : __uint_as_float(0x7fffffffu);
+                    y[u].y = fabsf(v[t].y) <= 3.4028235e38f ? v[t].y * s : __uint_as_float(0x7fffffffu);
                 }
+                w0[k >> 1] |= to_e4m3x2(y[0].x, y[1].x) << (16 * (k & 1));
+                w1[k >> 1] |= to_e4m3x2(y[0].y, y[1].y) << (16 * (k & 1));
+            }
+            unsigned char *dst = dst0 + (size_t)e * 16;
+            if (full) {
+                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                if (!one) reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (t >= g.t0 && t < g.t1) {
+                        const int o = byte_of(t);
+                        dst[o] = (unsigned char)(w0[o >> 2] >> (8 * (o & 3)));
+                        if (!one) dst[16 + o] = (unsigned char)(w1[o >> 2] >> (8 * (o & 3)));
+                    }
             }
         } else {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const int lo = max(g.t0 - 8 * hf, 0), hi = min(g.t1 - 8 * hf, 8);
-                if (lo >= hi) continue;
-                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(g.dst) + ((size_t)hf * E + e0) * 8;
-                const __nv_bfloat16 *tb = reinterpret_cast<const __nv_bfloat16 *>(tile) + hf * (kPiece * 8);
-                if (hi - lo == 8) {
-                    for (int i = tid; i < n; i += kThreads)
-                        reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(tb)[i];
+                __nv_bfloat16 r0[8], r1[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    r0[k] = __float2bfloat16_rn(v[8 * hf + k].x);
+                    r1[k] = __float2bfloat16_rn(v[8 * hf + k].y);
+                }
+                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(dst0) + ((size_t)hf * E + e) * 8;
+                if (g.t0 <= 8 * hf && g.t1 >= 8 * hf + 8) {
+                    uint4 u0, u1;
+                    memcpy(&u0, r0, 16);
+                    memcpy(&u1, r1, 16);
+                    reinterpret_cast<uint4 *>(dst)[0] = u0;
+                    if (!one) reinterpret_cast<uint4 *>(dst)[1] = u1;
                 } else {
-                    for (int i = tid; i < n * (hi - lo); i += kThreads) {
-                        const int o = (i / (hi - lo)) * 8 + lo + i % (hi - lo);
-                        dst[o] = tb[o];
-                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (8 * hf + k >= g.t0 && 8 * hf + k < g.t1) {
+                            dst[k] = r0[k];
+                            if (!one) dst[8 + k] = r1[k];
+                        }
                 }
             }
         }
     }
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) paged_read_kernel(WriteArgs a) {
-    __shared__ __align__(16) unsigned char tile[kPiece * (E4M3 ? 16 : 32)];
-    __shared__ __align__(16) unsigned char sc[32];
+// VEC: records start on 4-byte boundaries.
+template <bool E4M3, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads, 2) paged_read_kernel(WriteArgs a) {
     const bool is_k = blockIdx.y == 0;
     const int E = is_k ? a.ek : a.ev, A = is_k ? a.ak : a.av;
     Group g;
-    if (!my_group(a, is_k ? a.pool.k : a.pool.v, is_k ? a.pool.kg : a.pool.vg, g)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __nv_bfloat16 *rec = is_k ? a.kf : a.vf;
-    if (!g.dst) {
-        for (long long i = tid; i < (long long)(g.t1 - g.t0) * E; i += kThreads)
-            rec[(size_t)g.row0 * E + i] = __float2bfloat16_rn(0.f);
-        return;
+    if (!find_group(a, g)) return;
+    const unsigned char *const from = group_at(a, g, is_k ? a.pool.k : a.pool.v, is_k ? a.pool.kg : a.pool.vg);
+    const int tid = threadIdx.x, threads = blockDim.x;
+    __nv_bfloat16 *rec = (is_k ? a.kf : a.vf) + (size_t)g.row0 * E - (size_t)g.t0 * E;
+    uint32_t sa[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
+    if (E4M3 && from) {
+        const uint4 u = reinterpret_cast<const uint4 *>(from)[E], v = reinterpret_cast<const uint4 *>(from)[E + 1];
+        sa[0] = u.x, sa[1] = u.y, sa[2] = u.z, sa[3] = u.w;
+        sb[0] = v.x, sb[1] = v.y, sb[2] = v.z, sb[3] = v.w;
     }
-    if constexpr (E4M3) {
-        if (tid < 2) reinterpret_cast<uint4 *>(sc)[tid] = reinterpret_cast<const uint4 *>(g.dst)[E + tid];
-    }
-    for (int e0 = 0; e0 < E; e0 += kPiece) {
-        const int n = min(kPiece, E - e0);
-        if (e0) __syncthreads();
-        if constexpr (E4M3) {
-            for (int i = tid; i < n; i += kThreads)
-                reinterpret_cast<uint4 *>(tile)[i] = reinterpret_cast<const uint4 *>(g.dst)[e0 + i];
-        } else {
-            for (int i = tid; i < 2 * n; i += kThreads) {
-                const int hf = i >= n, e = hf ? i - n : i;
-                reinterpret_cast<uint4 *>(tile)[hf * kPiece + e] =
-                    reinterpret_cast<const uint4 *>(g.dst)[(size_t)hf * E + e0 + e];
+    for (int e = 2 * tid; e < E; e += 2 * threads) {
+        const bool one = e + 1 >= E;
+        // the two elements at slots k and k + 8 as fp32 (a page outside the pool: zeros)
+        uint32_t w[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) w[t] = 0u;
+        if (from) {
+            if constexpr (E4M3) {
+                const uint4 *row = reinterpret_cast<const uint4 *>(from) + e;
+                const uint4 u = row[0], v = one ? u : row[1];
+                const uint32_t c0[4] = {u.x, u.y, u.z, u.w}, c1[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 x0 = h2_to_f2(e4m3x2_to_h2(c0[k >> 1] >> (16 * (k & 1))));
+                    const float2 x1 = h2_to_f2(e4m3x2_to_h2(c1[k >> 1] >> (16 * (k & 1))));
+                    const uint32_t s0 = (e < A ? sa : sb)[k >> 1] >> (16 * (k & 1)),
+                                   s1 = (e + 1 < A ? sa : sb)[k >> 1] >> (16 * (k & 1));
+#pragma unroll
+                    for (int u2 = 0; u2 < 2; ++u2) {
+                        const float y0 = (u2 ? x0.y : x0.x) * exp_byte((s0 >> (8 * u2)) & 255u);
+                        const float y1 = (u2 ? x1.y : x1.x) * exp_byte((s1 >> (8 * u2)) & 255u);
+                        // exact in bf16: four significant bits
+                        w[k + 8 * u2] = (__float_as_uint(y0) >> 16) | (__float_as_uint(y1) & 0xffff0000u);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint4 *row = reinterpret_cast<const uint4 *>(from) + (size_t)hf * E + e;
+                    const uint4 u = row[0], v = one ? u : row[1];
+                    const uint32_t c0[4] = {u.x, u.y, u.z, u.w}, c1[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w[8 * hf + k] = __byte_perm(c0[k >> 1], c1[k >> 1], k & 1 ? 0x7632 : 0x5410);
+                }
             }
         }
-        __syncthreads();
-        for (int t = g.t0 + warp; t < g.t1; t += kWarps) {
-            __nv_bfloat16 *r = rec + (size_t)(g.row0 + t - g.t0) * E + e0;
-            for (int e = lane; e < n; e += 32) {
-                if constexpr (E4M3) {
-                    const float s = exp_byte(sc[(e0 + e >= A ? 16 : 0) + byte_of(t)]);
-                    const float2 f = h2_to_f2(e4m3x2_to_h2(tile[e * 16 + byte_of(t)]));
-                    r[e] = __float2bfloat16_rn(f.x * s);
-                } else {
-                    r[e] = reinterpret_cast<const __nv_bfloat16 *>(tile)[((t >> 3) * kPiece + e) * 8 + (t & 7)];
-                }
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            if (t < g.t0 || t >= g.t1) continue;
+            __nv_bfloat16 *r = rec + (size_t)t * E + e;
+            if (VEC) {
+                *reinterpret_cast<uint32_t *>(r) = w[t];
+            } else {
+                r[0] = __ushort_as_bfloat16((unsigned short)(w[t] & 0xffffu));
+                if (!one) r[1] = __ushort_as_bfloat16((unsigned short)(w[t] >> 16));
             }
         }
     }
@@ -289,6 +341,22 @@ WriteArgs write_args(const PagedShape &s, int batch, int n_rows, const int32_t *
     return a;
 }
 
+// Threads: one per pair of a record's elements (512 at most: longer records take several
+// pieces), so that short records leave few threads idle.
+int threads_of(const WriteArgs &a) {
+    const int pairs = (a.ek > a.ev ? a.ek : a.ev) / 2 + 1;
+    return std::min(kMaxThreads, (pairs + 31) / 32 * 32);
+}
+
+// Calls launch(e4m3, vec) as compile-time constants.
+template <class Launch>
+void by_format(bool e4m3, bool vec, Launch launch) {
+    if (e4m3)
+        vec ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
+    else
+        vec ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
+}
+
 // n rows of one sequence touch at most (n + 14) / 16 + 1 groups
 dim3 write_grid(int batch, int n_rows) {
     return dim3((unsigned)(((long long)n_rows + 14ll * batch) / 16 + batch), 2);
@@ -305,19 +373,11 @@ cudaError_t launch_paged_append(const PagedShape &s, int batch, int n_rows, cons
     a.kpool = static_cast<unsigned char *>(kpool);
     a.vpool = static_cast<unsigned char *>(vpool);
     const dim3 grid = write_grid(batch, n_rows);
-    // pairs of records and of their B parts start on 4-byte boundaries
     const bool vec = a.ek % 2 == 0 && a.ev % 2 == 0 && a.ak % 2 == 0 && a.av % 2 == 0;
-    if (s.pool.e4m3) {
-        if (vec)
-            paged_append_kernel<true, true><<<grid, kThreads, 0, st>>>(a, rope);
-        else
-            paged_append_kernel<true, false><<<grid, kThreads, 0, st>>>(a, rope);
-    } else {
-        if (vec)
-            paged_append_kernel<false, true><<<grid, kThreads, 0, st>>>(a, rope);
-        else
-            paged_append_kernel<false, false><<<grid, kThreads, 0, st>>>(a, rope);
-    }
+    const size_t smem = (size_t)(a.d2 / 2) * 16 * sizeof(float2);       // at most 16 KB
+    by_format(s.pool.e4m3 != 0, vec, [&](auto e4m3, auto v) {
+        paged_append_kernel<decltype(e4m3)::value, decltype(v)::value><<<grid, threads_of(a), smem, st>>>(a, rope);
+    });
     return cudaGetLastError();
 }
 
@@ -327,10 +387,9 @@ cudaError_t launch_paged_read(const PagedShape &s, int batch, int n_rows, const 
     a.kf = static_cast<__nv_bfloat16 *>(kf);
     a.vf = static_cast<__nv_bfloat16 *>(vf);
     const dim3 grid = write_grid(batch, n_rows);
-    if (s.pool.e4m3)
-        paged_read_kernel<true><<<grid, kThreads, 0, st>>>(a);
-    else
-        paged_read_kernel<false><<<grid, kThreads, 0, st>>>(a);
+    by_format(s.pool.e4m3 != 0, a.ek % 2 == 0 && a.ev % 2 == 0, [&](auto e4m3, auto v) {
+        paged_read_kernel<decltype(e4m3)::value, decltype(v)::value><<<grid, threads_of(a), 0, st>>>(a);
+    });
     return cudaGetLastError();
 }
 
