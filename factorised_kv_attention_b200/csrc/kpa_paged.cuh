@@ -114,6 +114,81 @@ __device__ __forceinline__ Found find_unit(int idx, const int32_t *cu, const int
     return hit;
 }
 
+// The same for row tiles of T rows in the order of what they cost: level 0 holds the last
+// tile of every sequence, level 1 the one before it, and so on, sequences in order within a
+// level, so that long rows start first and the last blocks are short.  i is the tile's index
+// from the sequence's front.  (Batches above 256 sequences: sequence after sequence, its last
+// tile first.)
+template <int T>
+__device__ __forceinline__ Found find_tile(int idx, const int32_t *cu, const int32_t *start, int batch, int n_rows,
+                                           int *err) {
+    if (batch > 256) {
+        Found f = find_unit(idx, cu, start, batch, n_rows, err, [](int, int n) { return (n + T - 1) / T; });
+        if (f.b >= 0) f.i = (f.n + T - 1) / T - 1 - f.i;
+        return f;
+    }
+    __shared__ Found hit;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int n[8], r0[8], pos[8], most = 0, all = 0;                 // sequences lane + 32 k
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int b = lane + 32 * k;
+            n[k] = r0[k] = pos[k] = 0;
+            if (b < batch) {
+                r0[k] = cu[b];
+                const int r1 = cu[b + 1];
+                pos[k] = start[b];
+                if (r0[k] < 0 || r1 < r0[k] || r1 > n_rows) {
+                    if (idx == 0) raise_error(err, kErrDeviceCheck);
+                } else {
+                    n[k] = r1 - r0[k];
+                }
+            }
+            const int t = (n[k] + T - 1) / T;
+            most = max(most, t);
+            all += t;
+        }
+        most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+        all = (int)__reduce_add_sync(0xffffffffu, (unsigned)all);
+        if (lane == 0) hit.b = -1;
+        __syncwarp();
+        if (idx < all) {
+            // the largest level whose first unit is no later than idx; before: units of the levels below
+            int lo = 0, hi = most, before = 0;                      // lo is one, hi is not
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                int c = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) c += min((n[k] + T - 1) / T, mid);
+                c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+                if (c <= idx) {
+                    lo = mid;
+                    before = c;
+                } else {
+                    hi = mid;
+                }
+            }
+            int rank = idx - before;                                // among the sequences that reach the level
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = (n[k] + T - 1) / T;
+                const unsigned m = __ballot_sync(0xffffffffu, t > lo);
+                if (t > lo && __popc(m & ((1u << lane) - 1u)) == rank) {
+                    hit.b = lane + 32 * k;
+                    hit.i = t - 1 - lo;
+                    hit.r0 = r0[k];
+                    hit.n = n[k];
+                    hit.pos = pos[k];
+                }
+                rank -= __popc(m);                                  // (negative once found)
+            }
+        }
+    }
+    __syncthreads();
+    return hit;
+}
+
 // ---- e4m3
 // two e4m3 codes (low byte first) as fp16x2
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {

@@ -146,6 +146,8 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
     st = device_info(&err, &sms);
     if (st != KPA_OK) return st;
     const AttnPlan p = plan_attn(s, batch, n_rows, chunks, max_len, window, sinks, sms);
+    // row tiles are blocks in y
+    if (chunks && n_rows / paged_mma_rows() + (int64_t)batch > 65535) return KPA_ERR_UNSUPPORTED;
     if (p.bytes > 0) {
         if (!workspace || ws_bytes < p.bytes) return KPA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return KPA_ERR_INVALID_ARG;

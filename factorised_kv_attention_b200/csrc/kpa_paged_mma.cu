@@ -121,22 +121,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const MmaArgs a)
     const int stage_bytes = G * (a.ekp + a.evp) * 16;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = blockIdx.y, split = blockIdx.z;
+    const int head = blockIdx.x, split = blockIdx.z;
     const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
 
     // ---- this CTA's rows: rows row0 .. row0 + n - 1, positions pos0 + r
     int b, row0, n;
     long long pos0;
     if (a.p.cu) {
-        const Found f = find_unit(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
-                                            [](int, int rows) { return (rows + kRows - 1) / kRows; });
+        const Found f = find_tile<kRows>(blockIdx.y, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err);
         if (f.b < 0) return;
         b = f.b;
         row0 = f.r0 + f.i * kRows;
         n = min(kRows, f.n - f.i * kRows);
         pos0 = (long long)f.pos + f.i * kRows;
     } else {
-        b = row0 = blockIdx.x;
+        b = row0 = blockIdx.y;
         n = 1;
         int len = a.p.seq_len[b];
         if (len < 0 || len > a.p.max_len) {
@@ -584,7 +583,8 @@ cudaError_t launch_paged_mma(const PagedShape &s, const PagedAttnArgs &p, cudaSt
     a.nch = (s.d.d2 + 3) / 4;
     const size_t smem = (size_t)smem_bytes(s.d, e4m3);
     const unsigned tiles = p.cu ? (unsigned)(((long long)p.n_rows + (long long)p.batch * (kRows - 1)) / kRows) : (unsigned)p.batch;
-    const dim3 grid(tiles, (unsigned)s.d.h, (unsigned)p.n_split);
+    // (y: at most 65535 row tiles, checked by the caller)
+    const dim3 grid((unsigned)s.d.h, tiles, (unsigned)p.n_split);
     cudaError_t e;
     if (sd.DH == 64)
         e = e4m3 ? launch_dh<64, true>(a, grid, smem, st) : launch_dh<64, false>(a, grid, smem, st);

@@ -119,16 +119,14 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = blockIdx.y, split = blockIdx.z;
+    const int head = blockIdx.x, split = blockIdx.z;
     const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
     const uint64_t limit = a.wait_limit_ns;
 
-    // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r; the last rows of a
-    // sequence, which see most, first
-    const Found f = find_unit(blockIdx.x, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err,
-                                        [](int, int rows) { return (rows + 2 * HQ - 1) / (2 * HQ); });
+    // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r
+    const Found f = find_tile<2 * HQ>(blockIdx.y, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err);
     if (f.b < 0) return;
-    const int b = f.b, q0 = ((f.n + 2 * HQ - 1) / (2 * HQ) - 1 - f.i) * 2 * HQ;
+    const int b = f.b, q0 = f.i * 2 * HQ;
     const int row0 = f.r0 + q0, n = min(2 * HQ, f.n - q0);
     const long long pos0 = (long long)f.pos + q0;
     if (tid == 0 && (pos0 < 0 || pos0 + n > a.p.max_len)) raise_error(a.p.err, kErrDeviceCheck);
@@ -151,21 +149,86 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     tp.n_kt = max(tp.last[0], tp.last[1]) + 1;
     auto seen = [&](int s) { return s <= hi && (s >= wstart || s < a.p.mask.sinks); };
 
-    if (tid == 0) {
-        for (int i = 0; i < C::NBAR; ++i) {
-            uint32_t count = 1;
-            if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2)) count = 4;
-            if ((i >= B_KST_EMPTY && i < B_KST_EMPTY + 2) || (i >= B_VST_EMPTY && i < B_VST_EMPTY + 2) ||
-                (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL)
-                count = kRebuildWarps;
-            mbar_init(bar(i), count);
+    // ---- producer's side: page lookups and copies
+    const int bg = a.box_groups, nb = TK / 16 / bg;               // boxes of a tile
+    const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
+    // lane i < nb: the first 16-slot group of box i of local tile t (-1: seen by no row)
+    auto lookup = [&](int t) -> long long {
+        if (lane >= nb || t >= tp.n_kt) return -1;
+        const int s0 = tl.slot_tile(v0 + t) * TK + lane * bg * 16;
+        if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return -1;
+        int entry, in;
+        split_group(a.pool, s0 >> 4, entry, in);
+        int page = __ldg(trow + entry);
+        if (page < 0 || page >= a.pool.n_pages) {
+            raise_error(a.p.err, kErrDeviceCheck);
+            page = 0;
         }
-        *abort_flag = 0;
-        mbar_fence_init();
-    }
+        return (long long)page * a.pool.pg + in;
+    };
+    // the head's factor slices of local tile t of a plane into its stage, which is free (a whole warp calls it)
+    auto copy_factors = [&](int t, bool is_v, long long grp) {
+        const int s = t % C::FST, ab = R * a.h1 * D1;             // ab: first B element of a record
+        const uint32_t full = bar((is_v ? B_VST_FULL : B_KST_FULL) + s);
+        const uint32_t st = smem_u32(smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
+        const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
+        const int rows = E4M3 ? bg : 2 * bg;                      // layout groups of a box
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
+        __syncwarp();
+        const CUtensorMap *map = is_v ? &tmv : &tmk;
+        for (int i = lane; i < ((C::NBLK * nb + 31) & ~31); i += 32) {
+            const int box = i % nb, k = i / nb;
+            const long long g = __shfl_sync(0xffffffffu, grp, box);
+            if (g < 0 || k >= C::NBLK) continue;
+            const int e = k < R ? k * a.h1 * D1 + i1 * D1
+                                : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8;
+            tma_load_2d(st + k * C::BOX + box * rows * 128, map, e * 4, (int)(E4M3 ? g : 2 * g), full);
+        }
+        if constexpr (E4M3) {                                     // the two scale rows of each group
+            const long long g = __shfl_sync(0xffffffffu, grp, (lane & 7) / bg);
+            if (lane < 8 && g >= 0) {
+                const int gb = is_v ? a.pool.vg : a.pool.kg;
+                const unsigned char *src = (is_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
+                sm100::bulk_g2s(st + C::FACT + lane * 32, src, 32, full);
+            }
+        }
+    };
+    long long next_grp = -1;                                      // lookup(1)
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
+    }
+    if (warp == kProducerWarp) {
+        // the first copies need none of the other warps: the query, then the first tile's factors
+        if (lane == 0) {
+            for (int i = 0; i < C::NBAR; ++i) {
+                uint32_t count = 1;
+                if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2)) count = 4;
+                if ((i >= B_KST_EMPTY && i < B_KST_EMPTY + 2) || (i >= B_VST_EMPTY && i < B_VST_EMPTY + 2) ||
+                    (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL)
+                    count = kRebuildWarps;
+                mbar_init(bar(i), count);
+            }
+            *abort_flag = 0;
+            mbar_fence_init();
+            if (tp.n_kt > 0) {
+                mbar_expect_tx(bar(B_Q), (uint32_t)((tp.act[0] ? 1 : 0) + (tp.act[1] ? 1 : 0)) * C::Q_HALF);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    if (tp.act[hh])
+#pragma unroll
+                        for (int cb = 0; cb < DH / 64; ++cb)
+                            tma_load_2d(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + cb * HQ * 128), &tmq,
+                                        head * DH + cb * 64, row0 + hh * HQ, bar(B_Q));
+            }
+        }
+        __syncwarp();
+        if (tp.n_kt > 0) {
+            const long long grp = lookup(0);
+            copy_factors(0, false, grp);
+            copy_factors(0, true, grp);
+            next_grp = lookup(1);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -193,81 +256,19 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     if (warp == kProducerWarp) {
         // ---------------------------------------------------------------- producer
         if (tp.n_kt > 0) {
-            if (lane == 0) {
-                tma_prefetch_desc(&tmq);
-                tma_prefetch_desc(&tmk);
-                tma_prefetch_desc(&tmv);
-            }
-            const int bg = a.box_groups, nb = TK / 16 / bg;       // boxes of a tile
-            const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
-            // lane i < nb: the first 16-slot group of box i of local tile t (-1: seen by no row)
-            auto lookup = [&](int t) -> long long {
-                if (lane >= nb || t >= tp.n_kt) return -1;
-                const int s0 = tl.slot_tile(v0 + t) * TK + lane * bg * 16;
-                if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return -1;
-                int entry, in;
-                split_group(a.pool, s0 >> 4, entry, in);
-                int page = __ldg(trow + entry);
-                if (page < 0 || page >= a.pool.n_pages) {
-                    raise_error(a.p.err, kErrDeviceCheck);
-                    page = 0;
-                }
-                return (long long)page * a.pool.pg + in;
-            };
-            const int ab = R * a.h1 * D1;                         // first B element of a record
-            int issued[2][2] = {{-1, -1}, {-1, -1}};              // [plane][stage]
+            int issued[2][2] = {{0, -1}, {0, -1}};                // [plane][stage]: last tile copied there
             auto issue = [&](int t, bool is_v, long long grp) -> bool {
                 const int s = t % C::FST;
                 const bool ok = !(t >= C::FST) || wait((is_v ? B_VST_EMPTY : B_KST_EMPTY) + s, ((t / C::FST) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) return false;
-                const uint32_t full = bar((is_v ? B_VST_FULL : B_KST_FULL) + s);
-                const uint32_t st = smem_u32(smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
-                const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
-                const int rows = E4M3 ? bg : 2 * bg;              // layout groups of a box
-                if (lane == 0)
-                    mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
-                __syncwarp();
-                const CUtensorMap *map = is_v ? &tmv : &tmk;
-                for (int i = lane; i < ((C::NBLK * nb + 31) & ~31); i += 32) {
-                    const int box = i % nb, k = i / nb;
-                    const long long g = __shfl_sync(0xffffffffu, grp, box);
-                    if (g < 0 || k >= C::NBLK) continue;
-                    const int e = k < R ? k * a.h1 * D1 + i1 * D1
-                                        : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8;
-                    tma_load_2d(st + k * C::BOX + box * rows * 128, map, e * 4, (int)(E4M3 ? g : 2 * g), full);
-                }
-                if constexpr (E4M3) {                             // the two scale rows of each group
-                    const long long g = __shfl_sync(0xffffffffu, grp, (lane & 7) / bg);
-                    if (lane < 8 && g >= 0) {
-                        const int gb = is_v ? a.pool.vg : a.pool.kg;
-                        const unsigned char *src =
-                            (is_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
-                        sm100::bulk_g2s(st + C::FACT + lane * 32, src, 32, full);
-                    }
-                }
+                copy_factors(t, is_v, grp);
                 issued[is_v ? 1 : 0][s] = t;
                 return true;
             };
-            long long grp = lookup(0);
-            // the first key tile's factors go out ahead of Q: its rebuild is the first step
-            bool ok = issue(0, false, grp);
-            const int nh = (tp.act[0] ? 1 : 0) + (tp.act[1] ? 1 : 0);
-            if (lane == 0) {
-                mbar_expect_tx(bar(B_Q), (uint32_t)nh * C::Q_HALF);
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    if (tp.act[hh])
-#pragma unroll
-                        for (int cb = 0; cb < DH / 64; ++cb)
-                            tma_load_2d(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + cb * HQ * 128), &tmq,
-                                        head * DH + cb * 64, row0 + hh * HQ, bar(B_Q));
-            }
-            __syncwarp();
-            long long next = lookup(1);
-            if (ok) ok = issue(0, true, grp);
+            bool ok = true;
             for (int t = 1; t < tp.n_kt && ok; ++t) {
-                grp = next;
-                next = lookup(t + 1);
+                const long long grp = next_grp;
+                next_grp = lookup(t + 1);
                 ok = issue(t, false, grp);
                 if (ok) ok = issue(t, true, grp);
             }
@@ -582,30 +583,46 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                         make_float2(live ? m_used : -INFINITY, live ? l_run : 0.f);
                     finite = !live || (l_run <= 3.4e38f && m_used <= 3.4e38f);
                 }
+                // Rows go out through the half's own query tile, which no product reads any more: a
+                // thread's row is strided by h d_h in memory, a row's 16-byte pieces by lanes are whole lines.
+                constexpr int kRow = DH * 2;                             // bytes of a bf16 row
+                unsigned char *stage = smem + C::OFF_Q + hh * C::Q_HALF + quarter * 32 * kRow;
 #pragma unroll 1
                 for (int c = 0; c < DH / 32; ++c) {
                     float v[32];
                     tmem_ld32(o_addr + c * 32, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * inv : 0.f;
                     if (exists) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * inv : 0.f;
-#pragma unroll
                         for (int j = 0; j < 32; ++j) finite &= fabsf(v[j]) <= 3.4e38f;
-                        if (whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                __nv_bfloat162 o2[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) o2[k] = __floats2bfloat162_rn(v[j + 2 * k], v[j + 2 * k + 1]);
-                                *reinterpret_cast<uint4 *>(a.p.out + rh * DH + c * 32 + j) = *reinterpret_cast<const uint4 *>(o2);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(a.p.part_o + (rh * a.p.n_split + split) * DH + c * 32 + j) =
-                                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                        }
                     }
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            __nv_bfloat162 o2[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o2[k] = __floats2bfloat162_rn(v[j + 2 * k], v[j + 2 * k + 1]);
+                            const int piece = (c * 32 + j) / 8;          // rotated by the lane: no bank conflicts
+                            *reinterpret_cast<uint4 *>(stage + lane * kRow + ((piece ^ (lane & 7)) << 4)) =
+                                *reinterpret_cast<const uint4 *>(o2);
+                        }
+                    } else if (exists) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(a.p.part_o + (rh * a.p.n_split + split) * DH + c * 32 + j) =
+                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
+                }
+                if (whole) {
+                    __syncwarp();
+                    constexpr int LPR = kRow / 16;                       // lanes per row
+                    const int piece = lane % LPR, first = quarter * 32 + hh * HQ;
+#pragma unroll 4
+                    for (int i = lane / LPR; i < 32; i += 32 / LPR)
+                        if (first + i < n)
+                            *reinterpret_cast<uint4 *>(a.p.out + ((size_t)(row0 + first + i) * h + head) * DH + piece * 8) =
+                                *reinterpret_cast<const uint4 *>(stage + i * kRow + ((piece ^ (i & 7)) << 4));
                 }
                 if (!finite) raise_error(a.p.err, kErrDeviceCheck);
             }
@@ -661,7 +678,7 @@ cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned lon
     cudaError_t e = ensure_dynamic_smem<paged_prefill_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)(((long long)p.n_rows + (long long)p.batch * (2 * HQ - 1)) / (2 * HQ));
-    paged_prefill_kernel<C><<<dim3(tiles, (unsigned)s.d.h, (unsigned)p.n_split), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
+    paged_prefill_kernel<C><<<dim3((unsigned)s.d.h, tiles, (unsigned)p.n_split), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.n_split == 1) return e;
     return launch_paged_combine(s, p, st);
