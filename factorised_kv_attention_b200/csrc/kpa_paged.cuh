@@ -211,6 +211,14 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t w) {
         : "r"(w));
     return f;
 }
+// Four e4m3 bytes of a group row or column pair, in the order slot, slot + 8 of one value,
+// then of the next: the two values of the lower slots and of the upper slots, as fp16x2.
+__device__ __forceinline__ void e4m3_split(uint32_t w, uint32_t &lower, uint32_t &upper) {
+    const uint32_t v = __byte_perm(w, 0, 0x3120);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lower), "=r"(upper)
+        : "r"(v));
+}
 // 2^(byte - 127) for byte in [1, 254]
 __device__ __forceinline__ float exp_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
 // Four slots' exponent bytes of the A row and of the B row (each in [63, 190] for a slot that

@@ -50,9 +50,9 @@ struct AttnPlan {
 };
 
 // How the rows' key range is split.
-//  - The chunk kernels: when there are fewer CTAs than two per SM, into as many runs as make
-//    up for it, of at least four tiles each: shorter ones cost more in partials than they
-//    gain.
+//  - The chunk kernels: with fewer CTAs than two per SM, into runs of at least four tiles
+//    (shorter ones cost more in partials than they gain), as many as make the last wave of
+//    CTAs end soonest when a CTA costs its tiles and three more.
 //  - The single-token kernel: one CTA per slot of the SMs for a single sequence; several
 //    sequences may have different lengths (the host does not see them), so up to four times
 //    as many shorter runs let the CTA scheduler even them out, as long as a run keeps eight
@@ -90,9 +90,17 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         const int kTile = p.tcgen05 ? 128 : 64;
         const int64_t row_tiles = chunks ? std::max<int64_t>((n_rows + tr - 1) / tr, std::min(batch, n_rows)) : batch;
         const int64_t ctas = std::max<int64_t>(1, row_tiles * d.h);
-        const int64_t s =
-            std::min((2 * (int64_t)sms + ctas - 1) / ctas, visible(kTile, chunks ? tr : 1) / kMinTiles);
-        p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(s, 4096));
+        const int64_t tiles = visible(kTile, chunks ? tr : 1);
+        int64_t best = 0;
+        p.n_split = 1;
+        if (ctas < 2 * (int64_t)sms)
+            for (int64_t k = 1; k <= std::min<int64_t>(4096, std::max<int64_t>(1, tiles / kMinTiles)) && ctas * k <= 4 * (int64_t)sms + ctas; ++k) {
+                const int64_t cost = ((ctas * k + sms - 1) / sms) * ((tiles + k - 1) / k + 3);
+                if (k == 1 || cost < best) {
+                    best = cost;
+                    p.n_split = (int)k;
+                }
+            }
     }
     const size_t rh = (size_t)n_rows * d.h * p.n_split;
     p.ml_off = (rh * d.dh * sizeof(float) + 255) & ~(size_t)255;

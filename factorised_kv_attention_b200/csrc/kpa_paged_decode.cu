@@ -147,15 +147,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t mask_pair(uint32_t v, bool k0, bool k1) {
     return (k0 ? (v & 0xffffu) : 0u) | (k1 ? (v & 0xffff0000u) : 0u);
 }
-// Four e4m3 bytes of a group row or column pair, in the order slot, slot + 8 of one value,
-// then of the next: the two values of the lower slots and of the upper slots, as fp16x2.
-__device__ __forceinline__ void e4m3_split(uint32_t w, uint32_t &lower, uint32_t &upper) {
-    const uint32_t v = __byte_perm(w, 0, 0x3120);
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lower), "=r"(upper)
-        : "r"(v));
-}
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const DecodeArgsP a) {
     constexpr int MA = C::MA, D1 = C::D1, D2 = C::D2, RK = C::RK, RV = C::RV, H2 = C::H2, H = C::H, DH = C::DH;

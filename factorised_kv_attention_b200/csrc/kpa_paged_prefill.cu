@@ -14,8 +14,8 @@
 //   - a tile's 16-slot groups come through the page table: the producer's lanes each load
 //     boxes of as many groups as a page surely holds together (1, 2, 4 or 8), and skip boxes
 //     that no row sees; rebuilt slots that no row sees are zeros;
-//   - an e4m3 token's two scales multiply into its A factors, in fp32, before K and V are
-//     rounded once to fp16.
+//   - an e4m3 token's two scales multiply into its factors before K and V are rounded once to
+//     fp16: in fp32, or at R = 2 in fp16, where factors and products are exact.
 #include <cstring>
 
 #include "kpa_f32x2.cuh"
@@ -56,6 +56,7 @@ template <int D2_, int R_, bool E4M3_>
 struct Cfg {
     static constexpr int D1 = 8, D2 = D2_, R = R_, DH = D1 * D2, HB = D2 / 8;
     static constexpr bool E4M3 = E4M3_;
+    static constexpr bool PAIRED = E4M3 && R == 2;             // the fp16 rebuild of two slots a lane
     static constexpr int NG = E4M3 ? TK / 16 : TK / 8;         // layout groups of a tile
     static constexpr int BOX = NG * 128;                       // 8 elements x the tile's slots
     static constexpr int NBLK = R * (1 + HB);                  // blocks of a plane: A_r, then (r, hb) of B
@@ -75,6 +76,17 @@ struct Cfg {
     static_assert(D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
     static_assert(ST % 128 == 0 && SMEM <= 226 * 1024, "shared memory (a little is static)");
 };
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 
 // mbarrier slots
 enum : int {
@@ -268,8 +280,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             bool ok = true;
             for (int t = 1; t < tp.n_kt && ok; ++t) {
                 const long long grp = next_grp;
-                next_grp = lookup(t + 1);
                 ok = issue(t, false, grp);
+                next_grp = lookup(t + 1);                         // (a round trip: not ahead of the copy)
                 if (ok) ok = issue(t, true, grp);
             }
             // every copy this warp started lands before the CTA can exit
@@ -345,6 +357,75 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             const uint32_t dst = smem_u32(smem + (is_v ? C::OFF_V : C::OFF_K + (t & 1) * C::KV_TILE));
             const int t0 = tl.slot_tile(v0 + t) * TK;
             const bool edge = !(t0 + TK - 1 <= hi && t0 >= wstart);
+            if constexpr (C::PAIRED) {
+                // One 16-slot group per warp, slots tok and tok + 8 (neighbouring bytes) per lane, in
+                // fp16: a code times half of its token's exponent is exact, so is the product of two
+                // (2^-25 where it leaves fp16's normal range), and the sum over the two ranks is
+                // rounded once.
+                const int lg = rw;
+                const unsigned char *grp = st + lg * 128, *e = st + C::FACT + lg * 32 + 2 * tok;
+                uint32_t sa2, sb_lo, sb_hi;                        // scales: A of both slots, B of each
+                {
+                    const uint32_t ea = *reinterpret_cast<const uint16_t *>(e), eb = *reinterpret_cast<const uint16_t *>(e + 16);
+                    const int x0 = (int)(((ea & 255u) + (eb & 255u) + 130u) & 255u) - 128;
+                    const int x1 = (int)(((ea >> 8) + (eb >> 8) + 130u) & 255u) - 128;
+                    auto half_exp = [](int x) { return __uint_as_float((uint32_t)(127 + x) << 23); };
+                    sa2 = pack_half2(half_exp(x0 >> 1), half_exp(x1 >> 1));
+                    const float b0 = half_exp(x0 - (x0 >> 1)), b1 = half_exp(x1 - (x1 >> 1));
+                    sb_lo = pack_half2(b0, b0);
+                    sb_hi = pack_half2(b1, b1);
+                }
+                uint32_t bw[4], blo[4], bhi[4];                    // block r * HB + hb: features of tok, of tok + 8
+                if constexpr (HB == 2) {
+                    ldsm_x4_t(smem_u32(grp + (R + blk) * C::BOX + brow * 16), bw);
+                } else {
+                    uint32_t b2[2];
+                    ldsm_x2_t(smem_u32(grp + (R + (blk & 1)) * C::BOX + brow * 16), b2);
+                    bw[0] = b2[0], bw[1] = b2[1], bw[2] = bw[3] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < R * HB; ++i) {
+                    e4m3_split(bw[i], blo[i], bhi[i]);
+                    blo[i] = hmul2(blo[i], sb_lo);
+                    bhi[i] = hmul2(bhi[i], sb_hi);
+                }
+                const bool zero_lo = edge && !seen(t0 + lg * 16 + tok), zero_hi = edge && !seen(t0 + lg * 16 + 8 + tok);
+                constexpr int JN = 4 / HB;
+#pragma unroll
+                for (int i = 0; i < 8 / JN; ++i) {
+                    uint32_t w[2][4];
+#pragma unroll
+                    for (int u = 0; u < JN; ++u) {
+                        uint32_t a_lo[R], a_hi[R];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const uint32_t x = hmul2(
+                                e4m3x2_to_h2(*reinterpret_cast<const uint16_t *>(grp + r * C::BOX + (i * JN + u) * 16 + 2 * tok)), sa2);
+                            a_lo[r] = __byte_perm(x, 0, 0x1010);
+                            a_hi[r] = __byte_perm(x, 0, 0x3232);
+                        }
+#pragma unroll
+                        for (int hb = 0; hb < HB; ++hb) {
+                            const uint32_t lo2 = hfma2(a_lo[1], blo[HB + hb], hmul2(a_lo[0], blo[hb]));
+                            const uint32_t hi2 = hfma2(a_hi[1], bhi[HB + hb], hmul2(a_hi[0], bhi[hb]));
+                            w[0][u * HB + hb] = zero_lo ? 0u : lo2;
+                            w[1][u * HB + hb] = zero_hi ? 0u : hi2;
+                        }
+                    }
+                    const int f0 = HB == 2 ? (2 * i + (blk >> 1)) * 16 + (blk & 1) * 8 : (4 * i + blk) * 8;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int g = 2 * lg + hf;
+                        if (!is_v)
+                            stsm_x4(dst + (f0 >> 6) * (TK * 128) + sw128_chunk(g * kGroup + brow, (f0 & 63) >> 3), w[hf][0],
+                                    w[hf][1], w[hf][2], w[hf][3]);
+                        else
+                            stsm_x4_t(dst + (g >> 3) * (DH * 128) + sw128_chunk(f0 + brow, g & 7), w[hf][0], w[hf][1],
+                                      w[hf][2], w[hf][3]);
+                    }
+                }
+                return;
+            }
 #pragma unroll 1
             for (int gi = 0; gi < TK / kGroup / kRebuildWarps; ++gi) {
                 const int g = rw * (TK / kGroup / kRebuildWarps) + gi;        // 8-slot group of the tile
