@@ -4,7 +4,7 @@
 //
 // The arrangement is the contiguous cache's prefill: one CTA takes 256 query rows of one
 // (sequence, head) as two 128-row halves that share every rebuilt 128-slot K/V tile and take
-// turns on the tensor pipe; a producer warp streams factor slices with TMA, eight warps
+// turns on the tensor pipe; a producer warp per plane streams factor slices with TMA, eight warps
 // rebuild K and V^T as fp16 in the 128-byte-swizzled layouts tcgen05.mma reads, one thread
 // issues S_h = Q_h K^T and O_h += P_h V, and eight softmax warps (a row per thread) turn S_h
 // into P_h in tensor memory (S0 | S1 | O0 | O1, 128 columns each).  What differs:
@@ -39,8 +39,8 @@ constexpr int TK = 128;                       // slots per tile
 constexpr int kSoftmaxWarps = 8, kRebuildWarps = 8;
 constexpr int kRebuildWarp0 = kSoftmaxWarps;
 constexpr int kMmaWarp = kSoftmaxWarps + kRebuildWarps;
-constexpr int kProducerWarp = kMmaWarp + 1;
-constexpr int kThreads = (kProducerWarp + 1) * 32;            // 576
+constexpr int kProducerWarp = kMmaWarp + 1;                   // keys; the next warp, values
+constexpr int kThreads = (kProducerWarp + 2) * 32;            // 608
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;           // the running maximum moves when it grew past 2^8
 
@@ -71,7 +71,7 @@ struct Cfg {
     static constexpr size_t OFF_KST = OFF_V + KV_TILE;
     static constexpr size_t OFF_VST = OFF_KST + (size_t)FST * ST;
     static constexpr size_t OFF_BAR = OFF_VST + (size_t)FST * ST;
-    static constexpr int NBAR = 24;
+    static constexpr int NBAR = 26;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
     static_assert(D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
     static_assert(ST % 128 == 0 && SMEM <= 226 * 1024, "shared memory (a little is static)");
@@ -104,6 +104,7 @@ enum : int {
     B_P_FULL = 19,     // +h
     B_O_FINAL = 21,    // +h
     B_DRAIN = 23,
+    B_P_HALF = 24,     // +h: the first half of P's columns
 };
 
 // Which local tiles a half works on: both start at 0; half h stops at last[h].
@@ -131,6 +132,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
     const int head = blockIdx.x, split = blockIdx.z;
     const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
     const uint64_t limit = a.wait_limit_ns;
@@ -161,61 +167,81 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     tp.n_kt = max(tp.last[0], tp.last[1]) + 1;
     auto seen = [&](int s) { return s <= hi && (s >= wstart || s < a.p.mask.sinks); };
 
-    // ---- producer's side: page lookups and copies
+    // ---- producers' side (one warp per plane): page lookups and copies
+    const bool is_producer = warp >= kProducerWarp, prod_v = warp == kProducerWarp + 1;
     const int bg = a.box_groups, nb = TK / 16 / bg;               // boxes of a tile
-    const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
-    // lane i < nb: the first 16-slot group of box i of local tile t (-1: seen by no row)
-    auto lookup = [&](int t) -> long long {
-        if (lane >= nb || t >= tp.n_kt) return -1;
+    const int rows = E4M3 ? bg : 2 * bg;                          // layout groups of a box
+    // lane i < nb: the page that holds box i of local tile t, not looked at yet, and the box's first
+    // 16-slot group inside it (-1: seen by no row)
+    int page = 0, in_page = -1;
+    auto fetch = [&](int t) {
+        in_page = -1;
+        if (lane >= nb || t >= tp.n_kt) return;
         const int s0 = tl.slot_tile(v0 + t) * TK + lane * bg * 16;
-        if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return -1;
-        int entry, in;
-        split_group(a.pool, s0 >> 4, entry, in);
-        int page = __ldg(trow + entry);
-        if (page < 0 || page >= a.pool.n_pages) {
-            raise_error(a.p.err, kErrDeviceCheck);
-            page = 0;
-        }
-        return (long long)page * a.pool.pg + in;
+        if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return;
+        int entry;
+        split_group(a.pool, s0 >> 4, entry, in_page);
+        page = __ldg(a.pool.table + (size_t)b * a.pool.table_stride + entry);
     };
-    // the head's factor slices of local tile t of a plane into its stage, which is free (a whole warp calls it)
-    auto copy_factors = [&](int t, bool is_v, long long grp) {
-        const int s = t % C::FST, ab = R * a.h1 * D1;             // ab: first B element of a record
-        const uint32_t full = bar((is_v ? B_VST_FULL : B_KST_FULL) + s);
-        const uint32_t st = smem_u32(smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
+    // copies of this lane: box (lane + 32 j) % nb of block (lane + 32 j) / nb
+    constexpr int CP = (C::NBLK * 8 + 31) / 32;
+    int cp_x[CP], cp_dst[CP], cp_box[CP];
+    if (is_producer) {
+        const int ab = R * a.h1 * D1;                             // first B element of a record
+#pragma unroll
+        for (int j = 0; j < CP; ++j) {
+            const int i = lane + 32 * j, k = i / nb;
+            cp_box[j] = i % nb;
+            cp_x[j] = k >= C::NBLK ? -1
+                      : 4 * (k < R ? k * a.h1 * D1 + i1 * D1
+                                   : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8);
+            cp_dst[j] = k * C::BOX + cp_box[j] * rows * 128;
+        }
+    }
+    // the head's factor slices of local tile t (its pages fetched) into its stage, which is free
+    auto copy_factors = [&](int t) {
+        long long grp = -1;
+        if (in_page >= 0) {
+            if (page < 0 || page >= a.pool.n_pages) {
+                raise_error(a.p.err, kErrDeviceCheck);
+                page = 0;
+            }
+            grp = (long long)page * a.pool.pg + in_page;
+        }
+        const int s = t % C::FST;
+        const uint32_t full = bar((prod_v ? B_VST_FULL : B_KST_FULL) + s);
+        const uint32_t st = smem_u32(smem + (prod_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
         const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
-        const int rows = E4M3 ? bg : 2 * bg;                      // layout groups of a box
         if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
         __syncwarp();
-        const CUtensorMap *map = is_v ? &tmv : &tmk;
-        for (int i = lane; i < ((C::NBLK * nb + 31) & ~31); i += 32) {
-            const int box = i % nb, k = i / nb;
-            const long long g = __shfl_sync(0xffffffffu, grp, box);
-            if (g < 0 || k >= C::NBLK) continue;
-            const int e = k < R ? k * a.h1 * D1 + i1 * D1
-                                : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8;
-            tma_load_2d(st + k * C::BOX + box * rows * 128, map, e * 4, (int)(E4M3 ? g : 2 * g), full);
+        const CUtensorMap *map = prod_v ? &tmv : &tmk;
+#pragma unroll
+        for (int j = 0; j < CP; ++j) {
+            const long long g = __shfl_sync(0xffffffffu, grp, cp_box[j]);
+            if (g >= 0 && cp_x[j] >= 0) tma_load_2d(st + cp_dst[j], map, cp_x[j], (int)(E4M3 ? g : 2 * g), full);
         }
         if constexpr (E4M3) {                                     // the two scale rows of each group
             const long long g = __shfl_sync(0xffffffffu, grp, (lane & 7) / bg);
             if (lane < 8 && g >= 0) {
-                const int gb = is_v ? a.pool.vg : a.pool.kg;
-                const unsigned char *src = (is_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
+                const int gb = prod_v ? a.pool.vg : a.pool.kg;
+                const unsigned char *src = (prod_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
                 sm100::bulk_g2s(st + C::FACT + lane * 32, src, 32, full);
             }
         }
     };
-    long long next_grp = -1;                                      // lookup(1)
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
+    if (is_producer) fetch(0);
     if (warp == kProducerWarp) {
-        // the first copies need none of the other warps: the query, then the first tile's factors
+        // the first copies need none of the other warps: the query, then the first key factors
         if (lane == 0) {
             for (int i = 0; i < C::NBAR; ++i) {
                 uint32_t count = 1;
-                if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2)) count = 4;
+                if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2) ||
+                    (i >= B_P_HALF && i < B_P_HALF + 2))
+                    count = 4;
                 if ((i >= B_KST_EMPTY && i < B_KST_EMPTY + 2) || (i >= B_VST_EMPTY && i < B_VST_EMPTY + 2) ||
                     (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL)
                     count = kRebuildWarps;
@@ -235,12 +261,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             }
         }
         __syncwarp();
-        if (tp.n_kt > 0) {
-            const long long grp = lookup(0);
-            copy_factors(0, false, grp);
-            copy_factors(0, true, grp);
-            next_grp = lookup(1);
-        }
+        if (tp.n_kt > 0) copy_factors(0);
     }
     tc_fence_before();
     __syncthreads();
@@ -265,33 +286,24 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         }
     };
 
-    if (warp == kProducerWarp) {
-        // ---------------------------------------------------------------- producer
+    if (is_producer) {
+        // ---------------------------------------------------------------- producers
         if (tp.n_kt > 0) {
-            int issued[2][2] = {{0, -1}, {0, -1}};                // [plane][stage]: last tile copied there
-            auto issue = [&](int t, bool is_v, long long grp) -> bool {
-                const int s = t % C::FST;
-                const bool ok = !(t >= C::FST) || wait((is_v ? B_VST_EMPTY : B_KST_EMPTY) + s, ((t / C::FST) - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) return false;
-                copy_factors(t, is_v, grp);
-                issued[is_v ? 1 : 0][s] = t;
-                return true;
-            };
-            bool ok = true;
-            for (int t = 1; t < tp.n_kt && ok; ++t) {
-                const long long grp = next_grp;
-                ok = issue(t, false, grp);
-                next_grp = lookup(t + 1);                         // (a round trip: not ahead of the copy)
-                if (ok) ok = issue(t, true, grp);
+            const int b_empty = prod_v ? B_VST_EMPTY : B_KST_EMPTY, b_full = prod_v ? B_VST_FULL : B_KST_FULL;
+            if (prod_v) copy_factors(0);
+            fetch(1);                                             // (waited for at its use)
+            int issued = 0;
+            for (int t = 1; t < tp.n_kt; ++t) {
+                const bool ok = t < C::FST || wait(b_empty + t % C::FST, ((t / C::FST) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                copy_factors(t);
+                issued = t;
+                fetch(t + 1);
             }
             // every copy this warp started lands before the CTA can exit
-            (void)mbar_wait(bar(B_Q), 0, limit);
-#pragma unroll
-            for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-                for (int s = 0; s < C::FST; ++s)
-                    if (issued[pl][s] >= 0)
-                        (void)mbar_wait(bar((pl ? B_VST_FULL : B_KST_FULL) + s), (issued[pl][s] / C::FST) & 1, limit);
+            if (!prod_v) (void)mbar_wait(bar(B_Q), 0, limit);
+            for (int t = max(0, issued - C::FST + 1); t <= issued; ++t)
+                (void)mbar_wait(bar(b_full + t % C::FST), (t / C::FST) & 1, limit);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
@@ -318,11 +330,15 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 return true;
             };
             auto issue_pv = [&](int hh, int t) -> bool {
-                if (!wait(B_P_FULL + hh, t & 1)) return false;
+                if (!wait(B_P_HALF + hh, t & 1)) return false;
                 if (hh == tp.first_half(t) && !wait(B_V_FULL, t & 1)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k) {
+                    if (k == TK / 32) {                               // the rest of P
+                        if (!wait(B_P_FULL + hh, t & 1)) return false;
+                        tc_fence_after();
+                    }
                     const uint64_t vd =
                         umma_desc_k_sw128(smem_u32(smem + C::OFF_V + (k / 4) * DH * 128)) + 2 * (k % 4);
                     umma_ts(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, vd, idesc_o, t > 0 || k > 0);
@@ -645,6 +661,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                         pw[jp] = pack_half2(p.x, p.y);
                     }
                     tmem_st16u(s_addr + c * 16, pw);                  // P over the S columns already read
+                    if (c == TK / 64 - 1) {                           // its products can start
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_P_HALF + hh));
+                    }
                 }
                 l_run += (suma.x + suma.y) + (sumb.x + sumb.y);
                 tmem_st_wait();
