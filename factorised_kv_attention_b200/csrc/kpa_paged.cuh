@@ -56,6 +56,16 @@ __device__ __forceinline__ Tiles visible_tiles(const Mask &m, int lo, int hi, in
     return t;
 }
 
+// Run `split` of n tiles cut into n_split runs that differ by at most one tile: [v0, v1).
+__device__ __forceinline__ void split_run(int n, int split, int n_split, int &v0, int &v1) {
+    v0 = 0, v1 = n;
+    if (n_split > 1) {
+        const int q = (int)((unsigned)n / (unsigned)n_split), r = n - q * n_split;
+        v0 = split * q + min(split, r);
+        v1 = v0 + q + (split < r ? 1 : 0);
+    }
+}
+
 // Finds the sequence that unit `idx` falls to when a sequence of n rows from position p has
 // count(p, n) units, laid one sequence after the other: its rows r0 .. r0 + n - 1, its first
 // position and the unit's index i inside it (b = -1 past the last unit).  Every thread of the

@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const MmaArgs a)
     if (a.p.cu && tid == 0 && (pos0 < 0 || pos0 + n > a.p.max_len)) raise_error(a.p.err, kErrDeviceCheck);
     Tiles tl = {0, 0, 0};
     if (lo <= hi) tl = visible_tiles(a.p.mask, lo, hi, kSlots);
-    const int v0 = (int)((long long)tl.n * split / a.p.n_split), v1 = (int)((long long)tl.n * (split + 1) / a.p.n_split);
+    int v0, v1;
+    split_run(tl.n, split, a.p.n_split, v0, v1);
     const int wstart = lo <= hi ? window_start(a.p.mask, lo) : 0;
     // seen by some row of the CTA
     auto seen = [&](int s) { return s <= hi && (s >= wstart || s < a.p.mask.sinks); };

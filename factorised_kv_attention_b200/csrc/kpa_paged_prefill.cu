@@ -154,7 +154,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     Tiles tl = {0, 0, 0};
     if (lo <= hi) tl = visible_tiles(a.p.mask, lo, hi, TK);
     const int wstart = lo <= hi ? window_start(a.p.mask, lo) : 0;
-    const int v0 = (int)((long long)tl.n * split / a.p.n_split), v1 = (int)((long long)tl.n * (split + 1) / a.p.n_split);
+    int v0, v1;
+    split_run(tl.n, split, a.p.n_split, v0, v1);
     TilePlan tp;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -186,18 +187,18 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     // copies of this lane: box (lane + 32 j) % nb of block (lane + 32 j) / nb
     constexpr int CP = (C::NBLK * 8 + 31) / 32;
     int cp_x[CP], cp_dst[CP], cp_box[CP];
-    if (is_producer) {
+    auto plan_copies = [&] {
         const int ab = R * a.h1 * D1;                             // first B element of a record
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
-            const int i = lane + 32 * j, k = i / nb;
-            cp_box[j] = i % nb;
+            const int i = lane + 32 * j, k = i >> (31 - __clz(nb));       // (nb is a power of two)
+            cp_box[j] = i & (nb - 1);
             cp_x[j] = k >= C::NBLK ? -1
                       : 4 * (k < R ? k * a.h1 * D1 + i1 * D1
                                    : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8);
             cp_dst[j] = k * C::BOX + cp_box[j] * rows * 128;
         }
-    }
+    };
     // the head's factor slices of local tile t (its pages fetched) into its stage, which is free
     auto copy_factors = [&](int t) {
         long long grp = -1;
@@ -261,8 +262,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             }
         }
         __syncwarp();
-        if (tp.n_kt > 0) copy_factors(0);
     }
+    if (is_producer) plan_copies();
+    if (warp == kProducerWarp && tp.n_kt > 0) copy_factors(0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
