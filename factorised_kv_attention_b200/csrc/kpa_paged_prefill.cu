@@ -1,6 +1,7 @@
 // kpa_paged_prefill.cu -- attention of chunks of new tokens over a paged factor cache on the
-// tcgen05 tensor cores, for d1 = 8 (d2 = 16 at R = 2 or 4, d2 = 8 at R = 2); every other
-// split runs on the mma.sync kernel.
+// tcgen05 tensor cores, for d1 = 8 (d2 = 16 at R = 2 or 4, d2 = 8 at R = 2) and d1 = 1, TPA's
+// split (d2 = 64 at R = 1 or 2, d2 = 128 at R = 2); every other split runs on the mma.sync
+// kernel.
 //
 // The arrangement is the contiguous cache's prefill: one CTA takes 256 query rows of one
 // (sequence, head) as two 128-row halves that share every rebuilt 128-slot K/V tile and take
@@ -14,6 +15,9 @@
 //   - a tile's 16-slot groups come through the page table: the producer's lanes each load
 //     boxes of as many groups as a page surely holds together (1, 2, 4 or 8), and skip boxes
 //     that no row sees; rebuilt slots that no row sees are zeros;
+//   - with d1 = 1 a head's slice of a slot (R (1 + d2) values) is larger than its key, so a
+//     tile is staged and rebuilt in units of 4096 / d_h slots, and as the slice's runs are
+//     long (16 d2 bytes) they come as bulk copies, one per lane;
 //   - an e4m3 token's two scales multiply into its factors before K and V are rounded once to
 //     fp16: in fp32, or at R = 2 in fp16, where factors and products are exact.
 #include <cstring>
@@ -52,29 +56,33 @@ struct PrefillArgsP {
     unsigned long long wait_limit_ns;
 };
 
-template <int D2_, int R_, bool E4M3_>
+template <int D1_, int D2_, int R_, bool E4M3_>
 struct Cfg {
-    static constexpr int D1 = 8, D2 = D2_, R = R_, DH = D1 * D2, HB = D2 / 8;
-    static constexpr bool E4M3 = E4M3_;
-    static constexpr bool PAIRED = E4M3 && R == 2;             // the fp16 rebuild of two slots a lane
-    static constexpr int NG = E4M3 ? TK / 16 : TK / 8;         // layout groups of a tile
-    static constexpr int BOX = NG * 128;                       // 8 elements x the tile's slots
-    static constexpr int NBLK = R * (1 + HB);                  // blocks of a plane: A_r, then (r, hb) of B
-    static constexpr int FACT = NBLK * BOX;                    // bytes of a stage, then 32 scale bytes a group
-    static constexpr int ST = FACT + (E4M3 ? NG * 32 : 0);
-    // factor stages: two where they fit beside the Q, K and V tiles, else one
-    static constexpr int FST = 2 * 2 * ST <= 56 * 1024 ? 2 : 1;
+    static constexpr int D1 = D1_, D2 = D2_, R = R_, DH = D1 * D2, HB = D2 / 8;
+    static constexpr bool E4M3 = E4M3_, TPA = D1 == 1;
+    static constexpr bool PAIRED = E4M3 && R <= 2;             // the fp16 rebuild of two slots a lane
     static constexpr uint32_t Q_HALF = HQ * DH * 2, KV_TILE = TK * DH * 2;
+    // A unit is what a factor stage holds: US slots in NG layout groups (8 slots, or 16 when e4m3).
+    static constexpr int US = TPA ? 4096 / DH : TK, NU = TK / US, NG = US / (E4M3 ? 16 : 8);
+    // d1 = 8: blocks of 8 elements x the unit's slots (A_r, then (r, hb) of B), then 32 scale bytes a
+    // group.  d1 = 1: per group R x (A row, D2 B rows) of 16 bytes, then its scale rows.
+    static constexpr int BOX = NG * 128, NBLK = R * (1 + HB), FACT = NBLK * BOX;
+    static constexpr int GROUP = R * (1 + D2) * 16 + (E4M3 ? 32 : 0);
+    static constexpr int ST = TPA ? NG * GROUP : FACT + (E4M3 ? NG * 32 : 0);
+    // factor stages of a plane: as many as fit beside the Q, K and V tiles (four at most)
     static constexpr size_t OFF_Q = 0;                         // two halves
     static constexpr size_t OFF_K = OFF_Q + 2 * Q_HALF;        // two buffers
     static constexpr size_t OFF_V = OFF_K + 2 * KV_TILE;       // one buffer
     static constexpr size_t OFF_KST = OFF_V + KV_TILE;
+    static constexpr size_t ROOM = 227 * 1024 - 256 - 1024 - 512 - OFF_KST;    // (static memory, alignment, barriers)
+    static constexpr int FST = ROOM >= 8 * (size_t)ST && TPA ? 4 : ROOM >= 4 * (size_t)ST ? 2 : 1;
     static constexpr size_t OFF_VST = OFF_KST + (size_t)FST * ST;
     static constexpr size_t OFF_BAR = OFF_VST + (size_t)FST * ST;
-    static constexpr int NBAR = 26;
+    static constexpr int NBAR = 34;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
-    static_assert(D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
-    static_assert(ST % 128 == 0 && SMEM <= 226 * 1024, "shared memory (a little is static)");
+    static_assert(TPA || D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
+    static_assert(!TPA || ((DH == 64 || DH == 128) && NG * R * 2 + (E4M3 ? NG : 0) <= 32), "a unit's copies, one per lane");
+    static_assert(ST % 16 == 0 && (TPA || ST % 128 == 0) && OFF_BAR % 8 == 0 && SMEM <= 227 * 1024 - 256, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -92,19 +100,19 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 enum : int {
     B_Q = 0,
     B_QREADY = 1,      // +h
-    B_KST_FULL = 3,    // +stage
-    B_VST_FULL = 5,
-    B_KST_EMPTY = 7,
-    B_VST_EMPTY = 9,
-    B_K_FULL = 11,     // +buffer
-    B_K_EMPTY = 13,
-    B_V_FULL = 15,
-    B_V_EMPTY = 16,
-    B_S_FULL = 17,     // +h
-    B_P_FULL = 19,     // +h
-    B_O_FINAL = 21,    // +h
-    B_DRAIN = 23,
-    B_P_HALF = 24,     // +h: the first half of P's columns
+    B_K_FULL = 3,      // +buffer
+    B_K_EMPTY = 5,
+    B_V_FULL = 7,
+    B_V_EMPTY = 8,
+    B_S_FULL = 9,      // +h
+    B_P_HALF = 11,     // +h: the first half of P's columns
+    B_P_FULL = 13,     // +h
+    B_O_FINAL = 15,    // +h
+    B_DRAIN = 17,
+    B_KST_FULL = 18,   // +stage
+    B_VST_FULL = 22,
+    B_KST_EMPTY = 26,
+    B_VST_EMPTY = 30,
 };
 
 // Which local tiles a half works on: both start at 0; half h stops at last[h].
@@ -121,7 +129,8 @@ template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgsP a) {
-    constexpr int D1 = C::D1, R = C::R, DH = C::DH, HB = C::HB;
+    constexpr int D1 = C::D1, R = C::R, DH = C::DH;
+    [[maybe_unused]] constexpr int HB = C::HB;
     constexpr bool E4M3 = C::E4M3;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -172,23 +181,40 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     const bool is_producer = warp >= kProducerWarp, prod_v = warp == kProducerWarp + 1;
     const int bg = a.box_groups, nb = TK / 16 / bg;               // boxes of a tile
     const int rows = E4M3 ? bg : 2 * bg;                          // layout groups of a box
-    // lane i < nb: the page that holds box i of local tile t, not looked at yet, and the box's first
-    // 16-slot group inside it (-1: seen by no row)
+    // The page of this lane's copies of unit u (d1 = 8: box `lane` of the tile; d1 = 1: its own copy's
+    // group), not looked at yet, and the first 16-slot group inside it (-1: nothing, or seen by no row)
+    constexpr int CPG = C::R * 2;                                 // d1 = 1: copies of a group, A and B per rank
+    const int my_group = !C::TPA ? lane : lane < C::NG * CPG ? lane / CPG : E4M3 ? lane - C::NG * CPG : C::NG;
     int page = 0, in_page = -1;
-    auto fetch = [&](int t) {
+    auto fetch = [&](int u) {
         in_page = -1;
-        if (lane >= nb || t >= tp.n_kt) return;
-        const int s0 = tl.slot_tile(v0 + t) * TK + lane * bg * 16;
-        if (s0 > hi || (s0 + bg * 16 <= wstart && s0 >= a.p.mask.sinks)) return;
+        const int t = u / C::NU;
+        if (my_group >= (C::TPA ? C::NG : nb) || t >= tp.n_kt) return;
+        const int span = C::TPA ? (E4M3 ? 16 : 8) : bg * 16;
+        const int s0 = tl.slot_tile(v0 + t) * TK + (u % C::NU) * C::US + my_group * span;
+        if (s0 > hi || (s0 + span <= wstart && s0 >= a.p.mask.sinks)) return;
         int entry;
         split_group(a.pool, s0 >> 4, entry, in_page);
         page = __ldg(a.pool.table + (size_t)b * a.pool.table_stride + entry);
     };
     // copies of this lane: box (lane + 32 j) % nb of block (lane + 32 j) / nb
-    constexpr int CP = (C::NBLK * 8 + 31) / 32;
+    // (d1 = 1: the lane's one copy: its offset in a 16-slot group of the pool, in the unit, and size)
+    constexpr int CP = C::TPA ? 1 : (C::NBLK * 8 + 31) / 32;
     int cp_x[CP], cp_dst[CP], cp_box[CP];
     auto plan_copies = [&] {
         const int ab = R * a.h1 * D1;                             // first B element of a record
+        if constexpr (C::TPA) {
+            const int gb = prod_v ? a.pool.vg : a.pool.kg;
+            const int c = lane % CPG, r = c >> 1;
+            if (lane >= C::NG * CPG) {                            // the scale rows
+                cp_x[0] = gb - 32, cp_dst[0] = my_group * C::GROUP + C::GROUP - 32, cp_box[0] = 32;
+            } else {
+                cp_x[0] = ((c & 1) ? ab + (r * a.h2 + i2) * C::D2 : r * a.h1 + i1) * 16 + (!E4M3 && (my_group & 1) ? gb / 2 : 0);
+                cp_dst[0] = my_group * C::GROUP + (r * (1 + C::D2) + (c & 1)) * 16;
+                cp_box[0] = (c & 1) ? C::D2 * 16 : 16;
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
             const int i = lane + 32 * j, k = i >> (31 - __clz(nb));       // (nb is a power of two)
@@ -199,8 +225,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             cp_dst[j] = k * C::BOX + cp_box[j] * rows * 128;
         }
     };
-    // the head's factor slices of local tile t (its pages fetched) into its stage, which is free
-    auto copy_factors = [&](int t) {
+    // the head's factor slices of unit u (its pages fetched) into its stage, which is free
+    auto copy_factors = [&](int u) {
         long long grp = -1;
         if (in_page >= 0) {
             if (page < 0 || page >= a.pool.n_pages) {
@@ -209,9 +235,19 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             }
             grp = (long long)page * a.pool.pg + in_page;
         }
-        const int s = t % C::FST;
+        const int s = u % C::FST;
         const uint32_t full = bar((prod_v ? B_VST_FULL : B_KST_FULL) + s);
         const uint32_t st = smem_u32(smem + (prod_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
+        if constexpr (C::TPA) {
+            const unsigned bytes = __reduce_add_sync(0xffffffffu, grp >= 0 ? (unsigned)cp_box[0] : 0u);
+            if (lane == 0) mbar_expect_tx(full, bytes);
+            __syncwarp();
+            if (grp >= 0)
+                sm100::bulk_g2s(st + cp_dst[0],
+                                (prod_v ? a.pool.v + (size_t)grp * a.pool.vg : a.pool.k + (size_t)grp * a.pool.kg) + cp_x[0],
+                                (uint32_t)cp_box[0], full);
+            return;
+        }
         const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
         if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
         __syncwarp();
@@ -240,12 +276,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         if (lane == 0) {
             for (int i = 0; i < C::NBAR; ++i) {
                 uint32_t count = 1;
-                if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_FULL && i < B_P_FULL + 2) ||
-                    (i >= B_P_HALF && i < B_P_HALF + 2))
-                    count = 4;
-                if ((i >= B_KST_EMPTY && i < B_KST_EMPTY + 2) || (i >= B_VST_EMPTY && i < B_VST_EMPTY + 2) ||
-                    (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL)
-                    count = kRebuildWarps;
+                if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_HALF && i < B_P_FULL + 2)) count = 4;
+                if (i >= B_KST_EMPTY || (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL) count = kRebuildWarps;
                 mbar_init(bar(i), count);
             }
             *abort_flag = 0;
@@ -295,17 +327,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             if (prod_v) copy_factors(0);
             fetch(1);                                             // (waited for at its use)
             int issued = 0;
-            for (int t = 1; t < tp.n_kt; ++t) {
-                const bool ok = t < C::FST || wait(b_empty + t % C::FST, ((t / C::FST) - 1) & 1);
+            for (int u = 1; u < tp.n_kt * C::NU; ++u) {
+                const bool ok = u < C::FST || wait(b_empty + u % C::FST, ((u / C::FST) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                copy_factors(t);
-                issued = t;
-                fetch(t + 1);
+                copy_factors(u);
+                issued = u;
+                fetch(u + 1);
             }
             // every copy this warp started lands before the CTA can exit
             if (!prod_v) (void)mbar_wait(bar(B_Q), 0, limit);
-            for (int t = max(0, issued - C::FST + 1); t <= issued; ++t)
-                (void)mbar_wait(bar(b_full + t % C::FST), (t / C::FST) & 1, limit);
+            for (int u = max(0, issued - C::FST + 1); u <= issued; ++u)
+                (void)mbar_wait(bar(b_full + u % C::FST), (u / C::FST) & 1, limit);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
@@ -368,31 +400,105 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const int rw = warp - kRebuildWarp0;
         const int tok = lane >> 2;                 // slot of the 8-slot group this lane holds
         const int blk = lane >> 3, brow = lane & 7;   // ldmatrix / stmatrix row this lane addresses
-        // One plane of local tile t: K (slot rows, stmatrix) or V^T (feature rows, stmatrix.trans).
-        auto rebuild = [&](int t, bool is_v) {
-            const int fs = t % C::FST;
+        // Unit j of one plane of local tile t: K (slot rows, stmatrix) or V^T (feature rows, stmatrix.trans).
+        auto rebuild = [&](int t, int j, bool is_v) {
+            const int fs = (t * C::NU + j) % C::FST;
             const unsigned char *st = smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)fs * C::ST;
             const uint32_t dst = smem_u32(smem + (is_v ? C::OFF_V : C::OFF_K + (t & 1) * C::KV_TILE));
             const int t0 = tl.slot_tile(v0 + t) * TK;
             const bool edge = !(t0 + TK - 1 <= hi && t0 >= wstart);
-            if constexpr (C::PAIRED) {
+            // the exact fp16 scales of an e4m3 group's slots tok and tok + 8 (scale rows at e): half of each
+            // token's exponent on A, half on B
+            auto paired_scales = [&](const unsigned char *e, uint32_t &sa2, uint32_t &sb_lo, uint32_t &sb_hi) {
+                const uint32_t ea = *reinterpret_cast<const uint16_t *>(e), eb = *reinterpret_cast<const uint16_t *>(e + 16);
+                const int x0 = (int)(((ea & 255u) + (eb & 255u) + 130u) & 255u) - 128;
+                const int x1 = (int)(((ea >> 8) + (eb >> 8) + 130u) & 255u) - 128;
+                auto half_exp = [](int x) { return __uint_as_float((uint32_t)(127 + x) << 23); };
+                sa2 = pack_half2(half_exp(x0 >> 1), half_exp(x1 >> 1));
+                const float b0 = half_exp(x0 - (x0 >> 1)), b1 = half_exp(x1 - (x1 >> 1));
+                sb_lo = pack_half2(b0, b0);
+                sb_hi = pack_half2(b1, b1);
+            };
+            // four 8-feature blocks of 8-slot group g from feature f_first on: this lane's words w, its block's
+            // first feature f0
+            auto store_blocks = [&](int g, int f0, const uint32_t (&w)[4]) {
+                if (!is_v)
+                    stsm_x4(dst + (f0 >> 6) * (TK * 128) + sw128_chunk(g * kGroup + brow, (f0 & 63) >> 3), w[0], w[1], w[2], w[3]);
+                else
+                    stsm_x4_t(dst + (g >> 3) * (DH * 128) + sw128_chunk(f0 + brow, g & 7), w[0], w[1], w[2], w[3]);
+            };
+            if constexpr (C::TPA && !E4M3) {
+                // one 8-slot group and 64 features per warp
+                constexpr int FP = 8 / C::NG;                      // warps per group
+                const int gu = rw / FP, fp = rw % FP, g = j * C::NG + gu;
+                const unsigned char *grp = st + gu * C::GROUP;
+                float av[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    av[r] = __uint_as_float(
+                        (uint32_t)(*reinterpret_cast<const uint16_t *>(grp + r * (1 + C::D2) * 16 + 2 * tok)) << 16);
+                const bool zero = edge && !seen(t0 + g * kGroup + tok);
+#pragma unroll
+                for (int q4 = 0; q4 < 2; ++q4) {
+                    const int f0 = fp * 64 + (q4 * 4 + blk) * 8;
+                    float2 acc[4];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        uint32_t bw[4];
+                        ldsm_x4_t(smem_u32(grp + (r * (1 + C::D2) + 1 + f0 + brow) * 16), bw);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 a2 = make_float2(av[r], av[r]), x = unpack_bf16x2(bw[i]);
+                            acc[i] = r == 0 ? fmul2(a2, x) : ffma2(a2, x, acc[i]);
+                        }
+                    }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = zero ? 0u : pack_half2(acc[i].x, acc[i].y);
+                    store_blocks(g, f0, w);
+                }
+                return;
+            }
+            if constexpr (C::TPA && E4M3) {
+                // one 16-slot group and 32 features per warp, slots tok and tok + 8 per lane (see below)
+                constexpr int FP = 8 / C::NG;
+                const int gu = rw / FP, fp = rw % FP, g = 2 * (j * C::NG + gu), f0 = fp * 32 + blk * 8;
+                const unsigned char *grp = st + gu * C::GROUP;
+                uint32_t sa2, sb_lo, sb_hi, w[2][4];
+                paired_scales(grp + C::GROUP - 32 + 2 * tok, sa2, sb_lo, sb_hi);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t x =
+                        hmul2(e4m3x2_to_h2(*reinterpret_cast<const uint16_t *>(grp + r * (1 + C::D2) * 16 + 2 * tok)), sa2);
+                    const uint32_t a_lo = __byte_perm(x, 0, 0x1010), a_hi = __byte_perm(x, 0, 0x3232);
+                    uint32_t bw[4];
+                    ldsm_x4_t(smem_u32(grp + (r * (1 + C::D2) + 1 + f0 + brow) * 16), bw);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t lo2, hi2;
+                        e4m3_split(bw[i], lo2, hi2);
+                        lo2 = hmul2(lo2, sb_lo);
+                        hi2 = hmul2(hi2, sb_hi);
+                        w[0][i] = r == 0 ? hmul2(a_lo, lo2) : hfma2(a_lo, lo2, w[0][i]);
+                        w[1][i] = r == 0 ? hmul2(a_hi, hi2) : hfma2(a_hi, hi2, w[1][i]);
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (edge && !seen(t0 + (g + hf) * kGroup + tok)) w[hf][0] = w[hf][1] = w[hf][2] = w[hf][3] = 0u;
+                    store_blocks(g + hf, f0, w[hf]);
+                }
+                return;
+            }
+            if constexpr (C::PAIRED && !C::TPA) {
                 // One 16-slot group per warp, slots tok and tok + 8 (neighbouring bytes) per lane, in
                 // fp16: a code times half of its token's exponent is exact, so is the product of two
                 // (2^-25 where it leaves fp16's normal range), and the sum over the two ranks is
                 // rounded once.
                 const int lg = rw;
                 const unsigned char *grp = st + lg * 128, *e = st + C::FACT + lg * 32 + 2 * tok;
-                uint32_t sa2, sb_lo, sb_hi;                        // scales: A of both slots, B of each
-                {
-                    const uint32_t ea = *reinterpret_cast<const uint16_t *>(e), eb = *reinterpret_cast<const uint16_t *>(e + 16);
-                    const int x0 = (int)(((ea & 255u) + (eb & 255u) + 130u) & 255u) - 128;
-                    const int x1 = (int)(((ea >> 8) + (eb >> 8) + 130u) & 255u) - 128;
-                    auto half_exp = [](int x) { return __uint_as_float((uint32_t)(127 + x) << 23); };
-                    sa2 = pack_half2(half_exp(x0 >> 1), half_exp(x1 >> 1));
-                    const float b0 = half_exp(x0 - (x0 >> 1)), b1 = half_exp(x1 - (x1 >> 1));
-                    sb_lo = pack_half2(b0, b0);
-                    sb_hi = pack_half2(b1, b1);
-                }
+                uint32_t sa2, sb_lo, sb_hi;
+                paired_scales(e, sa2, sb_lo, sb_hi);
                 uint32_t bw[4], blo[4], bhi[4];                    // block r * HB + hb: features of tok, of tok + 8
                 if constexpr (HB == 2) {
                     ldsm_x4_t(smem_u32(grp + (R + blk) * C::BOX + brow * 16), bw);
@@ -432,18 +538,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     }
                     const int f0 = HB == 2 ? (2 * i + (blk >> 1)) * 16 + (blk & 1) * 8 : (4 * i + blk) * 8;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int g = 2 * lg + hf;
-                        if (!is_v)
-                            stsm_x4(dst + (f0 >> 6) * (TK * 128) + sw128_chunk(g * kGroup + brow, (f0 & 63) >> 3), w[hf][0],
-                                    w[hf][1], w[hf][2], w[hf][3]);
-                        else
-                            stsm_x4_t(dst + (g >> 3) * (DH * 128) + sw128_chunk(f0 + brow, g & 7), w[hf][0], w[hf][1],
-                                      w[hf][2], w[hf][3]);
-                    }
+                    for (int hf = 0; hf < 2; ++hf) store_blocks(2 * lg + hf, f0, w[hf]);
                 }
                 return;
             }
+            if constexpr (C::TPA || C::PAIRED) return;
 #pragma unroll 1
             for (int gi = 0; gi < TK / kGroup / kRebuildWarps; ++gi) {
                 const int g = rw * (TK / kGroup / kRebuildWarps) + gi;        // 8-slot group of the tile
@@ -510,37 +609,30 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
 #pragma unroll
                 for (int i = 0; i < 8 / (4 / HB); ++i) {
                     const int f0 = HB == 2 ? (2 * i + (blk >> 1)) * 16 + (blk & 1) * 8 : (4 * i + blk) * 8;
-                    uint32_t w0, w1, w2, w3;
-                    if constexpr (HB == 2) {
-                        w0 = w[2 * i][0], w1 = w[2 * i][HB - 1], w2 = w[2 * i + 1][0], w3 = w[2 * i + 1][HB - 1];
-                    } else {
-                        w0 = w[4 * i][0], w1 = w[4 * i + 1][0], w2 = w[4 * i + 2][0], w3 = w[4 * i + 3][0];
-                    }
-                    if (!is_v) {
-                        const int row = g * kGroup + brow;                          // slot row
-                        const uint32_t ad = dst + (f0 >> 6) * (TK * 128) + sw128_chunk(row, (f0 & 63) >> 3);
-                        stsm_x4(ad, w0, w1, w2, w3);
-                    } else {
-                        const int row = f0 + brow;                                  // feature row
-                        const uint32_t ad = dst + (g >> 3) * (DH * 128) + sw128_chunk(row, g & 7);
-                        stsm_x4_t(ad, w0, w1, w2, w3);
-                    }
+                    uint32_t w4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w4[k] = HB == 2 ? w[2 * i + (k >> 1)][(k & 1) * (HB - 1)] : w[(4 * i + k) & 7][0];
+                    store_blocks(g, f0, w4);
                 }
             }
         };
         auto step = [&](int t, bool is_v) -> bool {
-            const int s = t & 1, fs = t % C::FST;           // K buffer, factor stage
-            bool ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (t / C::FST) & 1);
-            if (ok && !is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
-            if (ok && is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            rebuild(t, is_v);
+            const int s = t & 1;                            // K buffer
+            bool ok = true;
+            if (!is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
+            if (is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
+#pragma unroll 1
+            for (int j = 0; j < C::NU; ++j) {
+                const int u = t * C::NU + j, fs = u % C::FST;
+                if (ok) ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1);
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                rebuild(t, j, is_v);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
+            }
             fence_async_smem();        // visible to the tensor cores
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
-                mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
-            }
+            if (lane == 0) mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
             return true;
         };
         if (tp.n_kt > 0) {
@@ -773,7 +865,7 @@ cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned lon
     a.wait_limit_ns = wait_limit_ns;
     a.box_groups = 8;                            // as many groups as every aligned run of them shares a page
     while (s.pool.pg % a.box_groups != 0) a.box_groups /= 2;
-    CUtensorMap tmq, tmk, tmv;
+    CUtensorMap tmq, tmk, tmv;                   // (the planes' unused, but prefetched, at d1 = 1)
     const uint64_t sub = C::E4M3 ? 1 : 2, groups = (uint64_t)s.pool.n_pages * s.pool.pg * sub;
     const int rows = a.box_groups * (int)sub;
     if (!make_q_map(&tmq, p.q, (uint64_t)p.n_rows, (uint64_t)s.d.h * s.d.dh, HQ) ||
@@ -796,19 +888,27 @@ int paged_prefill_rows() { return 2 * HQ; }
 bool paged_prefill_supported(const PagedShape &s) {
     const Dims &d = s.d;
     // group coordinates of the tensor maps are 32-bit
-    if ((uint64_t)s.pool.n_pages * s.pool.pg * 2 > INT32_MAX) return false;
-    return d.d1 == 8 && d.rk == d.rv && ((d.d2 == 16 && (d.rk == 2 || d.rk == 4)) || (d.d2 == 8 && d.rk == 2));
+    if ((uint64_t)s.pool.n_pages * s.pool.pg * 2 > INT32_MAX || d.rk != d.rv) return false;
+    if (d.d1 == 1) return (d.d2 == 64 && d.rk <= 2) || (d.d2 == 128 && d.rk == 2);
+    return d.d1 == 8 && ((d.d2 == 16 && (d.rk == 2 || d.rk == 4)) || (d.d2 == 8 && d.rk == 2));
 }
 
 cudaError_t launch_paged_prefill(const PagedShape &s, const PagedAttnArgs &a, unsigned long long wait_limit_ns,
                                  cudaStream_t st) {
     if (!paged_prefill_supported(s)) return cudaErrorInvalidValue;
-    const bool q8 = s.pool.e4m3 != 0;
-    if (s.d.d2 == 8)
-        return q8 ? launch_cfg<Cfg<8, 2, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<8, 2, false>>(s, a, wait_limit_ns, st);
-    if (s.d.rk == 4)
-        return q8 ? launch_cfg<Cfg<16, 4, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<16, 4, false>>(s, a, wait_limit_ns, st);
-    return q8 ? launch_cfg<Cfg<16, 2, true>>(s, a, wait_limit_ns, st) : launch_cfg<Cfg<16, 2, false>>(s, a, wait_limit_ns, st);
+    const Dims &d = s.d;
+#define KPA_PREFILL_CASE(D1, D2, R)                                                             \
+    if (d.d1 == D1 && d.d2 == D2 && d.rk == R)                                                  \
+        return s.pool.e4m3 ? launch_cfg<Cfg<D1, D2, R, true>>(s, a, wait_limit_ns, st)          \
+                           : launch_cfg<Cfg<D1, D2, R, false>>(s, a, wait_limit_ns, st);
+    KPA_PREFILL_CASE(8, 16, 2)
+    KPA_PREFILL_CASE(8, 16, 4)
+    KPA_PREFILL_CASE(8, 8, 2)
+    KPA_PREFILL_CASE(1, 64, 1)
+    KPA_PREFILL_CASE(1, 64, 2)
+    KPA_PREFILL_CASE(1, 128, 2)
+#undef KPA_PREFILL_CASE
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace kpa
