@@ -88,7 +88,8 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
     } else {
         constexpr int kMinTiles = 4;
         const int kTile = p.tcgen05 ? 128 : 64;
-        const int64_t row_tiles = chunks ? std::max<int64_t>((n_rows + tr - 1) / tr, std::min(batch, n_rows)) : batch;
+        // (the rows of a sequence are not known here: half a tile of each is taken as empty)
+        const int64_t row_tiles = chunks ? (n_rows + (int64_t)std::min(batch, n_rows) * (tr / 2) + tr - 1) / tr : batch;
         const int64_t ctas = std::max<int64_t>(1, row_tiles * d.h);
         const int64_t tiles = visible(kTile, chunks ? tr : 1);
         int64_t best = 0;

@@ -478,8 +478,8 @@ int smem_bytes(const Dims &d, bool e4m3) {
 
 // out[row][head] = out_scale * sum_z 2^(m_z - M) o_z / sum_z 2^(m_z - M) l_z over the splits of
 // a row; a split that saw nothing (m = -inf, l = 0) is not read.  W warps share a (row, head):
-// one when there are few splits, eight (a whole block) when there are many, so that the loads
-// of a long list run side by side.
+// one when there are few splits or many rows, eight (a whole block) for many splits of few
+// rows, so that the loads of a long list run side by side.
 template <int W>
 __global__ void __launch_bounds__(256) paged_combine_kernel(PagedAttnArgs a, int h, int dh) {
     __shared__ float part[8][128 + 1];                              // features, then l
@@ -537,7 +537,7 @@ bool paged_mma_supported(const Dims &d, bool e4m3) {
 
 cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st) {
     const long long rh = (long long)a.n_rows * s.d.h;
-    const bool wide = a.n_split > 8;
+    const bool wide = a.n_split > 8 && rh < 1024;            // (more rows fill the SMs with a warp each)
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(wide ? rh : (rh + 7) / 8));
     lc.blockDim = dim3(256);
