@@ -21,6 +21,7 @@
 //   - an e4m3 token's two scales multiply into its factors before K and V are rounded once to
 //     fp16: in fp32, or at R = 2 in fp16, where factors and products are exact.
 #include <cstring>
+#include <type_traits>
 
 #include "kpa_f32x2.cuh"
 #include "kpa_paged.cuh"
@@ -401,7 +402,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const int tok = lane >> 2;                 // slot of the 8-slot group this lane holds
         const int blk = lane >> 3, brow = lane & 7;   // ldmatrix / stmatrix row this lane addresses
         // Unit j of one plane of local tile t: K (slot rows, stmatrix) or V^T (feature rows, stmatrix.trans).
-        auto rebuild = [&](int t, int j, bool is_v) {
+        auto rebuild = [&](int t, auto j_c, auto v_c) {
+            constexpr int j = decltype(j_c)::value;
+            constexpr bool is_v = decltype(v_c)::value;
             const int fs = (t * C::NU + j) % C::FST;
             const unsigned char *st = smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)fs * C::ST;
             const uint32_t dst = smem_u32(smem + (is_v ? C::OFF_V : C::OFF_K + (t & 1) * C::KV_TILE));
@@ -616,32 +619,44 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 }
             }
         };
-        auto step = [&](int t, bool is_v) -> bool {
-            const int s = t & 1;                            // K buffer
+        // unit j of a plane of tile t: its factors landed, and (first unit) the products over the tile it
+        // replaces done
+        auto unit = [&](int t, auto j_c, auto v_c) -> bool {
+            constexpr int j = decltype(j_c)::value;
+            constexpr bool is_v = decltype(v_c)::value;
+            const int s = t & 1, u = t * C::NU + j, fs = u % C::FST;      // K buffer, factor stage
             bool ok = true;
-            if (!is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
-            if (is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
-#pragma unroll 1
-            for (int j = 0; j < C::NU; ++j) {
-                const int u = t * C::NU + j, fs = u % C::FST;
-                if (ok) ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1);
-                if (!__all_sync(0xffffffffu, ok)) return false;
-                rebuild(t, j, is_v);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
-            }
-            fence_async_smem();        // visible to the tensor cores
+            if (j == 0 && !is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
+            if (j == 0 && is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
+            if (ok) ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            rebuild(t, j_c, v_c);
+            if (j == C::NU - 1) fence_async_smem();         // visible to the tensor cores
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
+            if (lane == 0) {
+                mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
+                if (j == C::NU - 1) mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
+            }
             return true;
         };
-        if (tp.n_kt > 0) {
-            bool ok = step(0, false);
-            for (int t = 0; t < tp.n_kt && ok; ++t) {
-                if (t + 1 < tp.n_kt) ok = step(t + 1, false);
-                if (ok) ok = step(t, true);
+        // the units of K of tile tk and of V of tile tv in turn (a plane's next copy lands while the
+        // other plane's unit is rebuilt); a tile past the last, or below 0, is skipped
+        auto both = [&](int tk, int tv) -> bool {
+            bool ok = true;
+            auto at = [&](auto j_c) {
+                if (ok && tk < tp.n_kt) ok = unit(tk, j_c, std::false_type{});
+                if (ok && tv >= 0) ok = unit(tv, j_c, std::true_type{});
+            };
+            at(std::integral_constant<int, 0>{});
+            if constexpr (C::NU > 1) at(std::integral_constant<int, 1>{});
+            if constexpr (C::NU > 2) {
+                at(std::integral_constant<int, 2>{});
+                at(std::integral_constant<int, 3>{});
             }
-        }
+            return ok;
+        };
+        bool ok = tp.n_kt > 0;
+        for (int t = -1; t < tp.n_kt && ok; ++t) ok = both(t + 1, t);
     } else {
         // ---------------------------------------------------------------- softmax rows
         const int hh = warp >> 2, quarter = warp & 3;
