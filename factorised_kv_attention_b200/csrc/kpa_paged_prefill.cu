@@ -402,8 +402,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const int tok = lane >> 2;                 // slot of the 8-slot group this lane holds
         const int blk = lane >> 3, brow = lane & 7;   // ldmatrix / stmatrix row this lane addresses
         // Unit j of one plane of local tile t: K (slot rows, stmatrix) or V^T (feature rows, stmatrix.trans).
-        auto rebuild = [&](int t, auto j_c, auto v_c) {
-            constexpr int j = decltype(j_c)::value;
+        auto rebuild = [&](int t, int j, auto v_c) {
             constexpr bool is_v = decltype(v_c)::value;
             const int fs = (t * C::NU + j) % C::FST;
             const unsigned char *st = smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)fs * C::ST;
@@ -621,8 +620,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         };
         // unit j of a plane of tile t: its factors landed, and (first unit) the products over the tile it
         // replaces done
-        auto unit = [&](int t, auto j_c, auto v_c) -> bool {
-            constexpr int j = decltype(j_c)::value;
+        auto unit = [&](int t, int j, auto v_c) -> bool {
             constexpr bool is_v = decltype(v_c)::value;
             const int s = t & 1, u = t * C::NU + j, fs = u % C::FST;      // K buffer, factor stage
             bool ok = true;
@@ -630,7 +628,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             if (j == 0 && is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
             if (ok) ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            rebuild(t, j_c, v_c);
+            rebuild(t, j, v_c);
             if (j == C::NU - 1) fence_async_smem();         // visible to the tensor cores
             __syncwarp();
             if (lane == 0) {
@@ -643,15 +641,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         // other plane's unit is rebuilt); a tile past the last, or below 0, is skipped
         auto both = [&](int tk, int tv) -> bool {
             bool ok = true;
-            auto at = [&](auto j_c) {
-                if (ok && tk < tp.n_kt) ok = unit(tk, j_c, std::false_type{});
-                if (ok && tv >= 0) ok = unit(tv, j_c, std::true_type{});
-            };
-            at(std::integral_constant<int, 0>{});
-            if constexpr (C::NU > 1) at(std::integral_constant<int, 1>{});
-            if constexpr (C::NU > 2) {
-                at(std::integral_constant<int, 2>{});
-                at(std::integral_constant<int, 3>{});
+#pragma unroll 1
+            for (int j = 0; j < C::NU && ok; ++j) {         // (not unrolled: the roles share the instruction cache)
+                if (tk < tp.n_kt) ok = unit(tk, j, std::false_type{});
+                if (ok && tv >= 0) ok = unit(tv, j, std::true_type{});
             }
             return ok;
         };
