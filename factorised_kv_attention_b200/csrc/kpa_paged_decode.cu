@@ -70,7 +70,8 @@ struct Cfg {
     static constexpr size_t SMEM = OFF_FLAGS + 4 * (1 + STAGES);
     static_assert(MA % (16 * HS) == 0 && (KPA || (D1 == 1 && H2 == 1)) && (!KPA || HS == 1), "shape");
     static_assert(D2 % 16 == 0 || (KPA && D2 == 8), "d2");
-    static_assert(WARPS <= 16 && STAGES * TG <= 32, "one warp issues the first ring");
+    static constexpr int FIRST = (STAGES * TG + 31) / 32;          // groups of the first ring per lane of a warp
+    static_assert(WARPS <= 16 && TG <= 32, "one warp issues a tile");
     static_assert((size_t)SLICES * H * (MO_LD + 2) * 4 <= (size_t)STAGES * STAGE_BYTES, "slice merge fits in the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -177,10 +178,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     // without a window the first ring's table entries do not depend on the length: fetch them
     // beside it (inside the row for every slot below max_len)
     const int v0 = split * a.gps;
-    int first_entry = -1, first_page = 0, first_in = 0;
-    if (warp == 0 && lane < STAGES * TG && a.p.mask.window == 0 && (long long)(v0 + lane) * 16 < a.p.max_len) {
-        split_group(a.pool, v0 + lane, first_entry, first_in);
-        first_page = __ldg(trow + first_entry);
+    int first_page[C::FIRST], first_in[C::FIRST];
+    const bool early = a.p.mask.window == 0;
+#pragma unroll
+    for (int k = 0; k < C::FIRST; ++k) {
+        const int i = lane + 32 * k;
+        if (warp == 0 && early && i < STAGES * TG && (long long)(v0 + i) * 16 < a.p.max_len) {
+            int entry;
+            split_group(a.pool, v0 + i, entry, first_in[k]);
+            first_page[k] = __ldg(trow + entry);
+        }
     }
     // query fragments (A operand): row g (g + 8) of tile mt is (i1, j1) = (2 mt + (g >> 2), 2 (g & 3)) and
     // (i1, j1 + 1) with d1 = 8, head 16 mt + g (+ 8) with d1 = 1
@@ -239,15 +246,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         bulk_g2s(dst + KG, a.pool.v + group * VG, VG, full0 + 8 * stage);
     };
     auto groups_in = [&](int t) { return min(TG, v1 - v0 - t * TG); };
-    if (warp == 0) {                                       // the first ring: one lane per group
+    if (warp == 0) {                                       // the first ring, a lane per group
         if (lane < STAGES && lane < n_tiles) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
         __syncwarp();
-        if (lane < STAGES * TG && v0 + lane < v1) {
-            if (first_entry < 0) {
-                split_group(a.pool, tl.slot_tile(v0 + lane), first_entry, first_in);
-                first_page = __ldg(trow + first_entry);
+#pragma unroll
+        for (int k = 0; k < C::FIRST; ++k) {
+            const int i = lane + 32 * k;
+            if (i < STAGES * TG && v0 + i < v1) {
+                if (!early) {
+                    int entry;
+                    split_group(a.pool, tl.slot_tile(v0 + i), entry, first_in[k]);
+                    first_page[k] = __ldg(trow + entry);
+                }
+                copy_group(i / TG, i % TG, group_index(first_page[k], first_in[k]));
             }
-            copy_group(lane / TG, lane % TG, group_index(first_page, first_in));
         }
     }
 
