@@ -140,10 +140,25 @@ def _addr(x):
     return x.data_ptr()
 
 
+def _current_stream():
+    """Handle of torch's current stream on the current device."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def _current_stream():
+            return torch.cuda.current_stream().cuda_stream
+    else:                                  # a tenth of the time that building a Stream object takes
+        device = torch.cuda.current_device
+
+        def _current_stream():
+            return raw(device())
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
