@@ -286,7 +286,9 @@ cudaError_t launch_paged_prefill(const PagedShape &s, const PagedAttnArgs &a, un
 // them), the 16-slot groups of its tiles and its CTAs per SM, and its launcher.
 int paged_decode_variant(const Dims &d);
 void paged_decode_shape(int variant, bool e4m3, int *tile_groups, int *ctas_per_sm);
+constexpr int kPagedMaxCluster = 16;
+int paged_decode_max_clusters(int variant, bool e4m3, int size);     // resident at once (at least 2 CTAs each)
 cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &a, int groups_per_split,
-                                unsigned long long wait_limit_ns, cudaStream_t st);
+                                bool cluster, unsigned long long wait_limit_ns, cudaStream_t st);
 
 }  // namespace kpa

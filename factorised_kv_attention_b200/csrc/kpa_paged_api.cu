@@ -45,6 +45,7 @@ struct AttnPlan {
     int variant;                 // of the single-token kernel, or -1: a chunk kernel
     bool tcgen05;                // (chunk kernels) the tcgen05 one
     int groups_per_split;        // (single-token kernel)
+    bool cluster;                // (single-token kernel) a sequence's splits merge in a cluster: no workspace
     int n_split;
     size_t ml_off, bytes;
 };
@@ -83,6 +84,18 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
                     break;
                 }
             }
+        // A sequence's splits merge in one cluster, without a second kernel, where every CTA is resident at
+        // once (a cluster holds its SMs until its longest split ends) and the splits get no more than two
+        // tiles or a quarter longer for it: the second kernel and its launch cost about as much.
+        const int64_t most = std::min<int64_t>(kPagedMaxCluster, (int64_t)sms * per_sm / batch);
+        for (int64_t t = per; t <= std::max(per + 2, per + per / 4) && most > 1; ++t) {
+            const int64_t n = (tiles + t - 1) / t;
+            if (n > 1 && n <= most && paged_decode_max_clusters(p.variant, e4m3, (int)n) >= batch) {
+                per = t;
+                p.cluster = true;
+                break;
+            }
+        }
         p.groups_per_split = (int)(per * tg);
         p.n_split = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
     } else {
@@ -105,7 +118,7 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
     }
     const size_t rh = (size_t)n_rows * d.h * p.n_split;
     p.ml_off = (rh * d.dh * sizeof(float) + 255) & ~(size_t)255;
-    p.bytes = p.n_split > 1 ? p.ml_off + ((rh * 2 * sizeof(float) + 255) & ~(size_t)255) : 0;
+    p.bytes = p.n_split > 1 && !p.cluster ? p.ml_off + ((rh * 2 * sizeof(float) + 255) & ~(size_t)255) : 0;
     return p;
 }
 
@@ -183,7 +196,7 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.ml_off);
     }
     a.err = err;
-    const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split,
+    const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split, p.cluster,
                                                                device_wait_limit_ns(), (cudaStream_t)stream)
                           : p.tcgen05      ? launch_paged_prefill(s, a, device_wait_limit_ns(), (cudaStream_t)stream)
                                            : launch_paged_mma(s, a, (cudaStream_t)stream);

@@ -26,7 +26,11 @@
 #include "kpa_paged.cuh"
 #include "kpa_sm100.cuh"
 
+#include <cooperative_groups.h>
+
 #include <type_traits>
+
+namespace cg = cooperative_groups;
 
 namespace kpa {
 namespace {
@@ -45,6 +49,7 @@ struct DecodeArgsP {
     PagedAttnArgs p;
     Pool pool;
     int gps;                      // 16-slot groups per split
+    int cluster;                  // the splits of a sequence are one cluster and merge over shared memory
     unsigned long long limit_ns;
 };
 
@@ -72,7 +77,8 @@ struct Cfg {
     static_assert(D2 % 16 == 0 || (KPA && D2 == 8), "d2");
     static constexpr int FIRST = (STAGES * TG + 31) / 32;          // groups of the first ring per lane of a warp
     static_assert(WARPS <= 16 && TG <= 32, "one warp issues a tile");
-    static_assert((size_t)SLICES * H * (MO_LD + 2) * 4 <= (size_t)STAGES * STAGE_BYTES, "slice merge fits in the ring");
+    static_assert((size_t)(SLICES * H * (MO_LD + 2) + H * (DH + 2)) * 4 <= (size_t)STAGES * STAGE_BYTES,
+                  "slice merge and merged partial fit in the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -219,14 +225,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     if (len > 0) tl = visible_tiles(a.p.mask, pos, pos, 16);
     const int wstart = len > 0 ? window_start(a.p.mask, pos) : 0;
     const int v1 = min(tl.n, v0 + a.gps);
+    float *mo = reinterpret_cast<float *>(smem), *mm = mo + SLICES * H * C::MO_LD;      // (after the loop)
+    float *merged = mm + SLICES * H * 2;                   // [H][DH] o, [H] m, [H] l: this CTA's, for its cluster
+    // the cluster's partials joined: each CTA a run of the outputs.  Every CTA of a cluster comes here.
+    auto join_cluster = [&] {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        const int n_cl = a.p.n_split, per = (H * DH / 4 + n_cl - 1) / n_cl;
+        const int lo = split * per, hi = min(H * DH / 4, lo + per);
+        for (int i4 = lo + tid; i4 < hi; i4 += C::THREADS) {
+            const int head = i4 * 4 / DH;
+            float M = -INFINITY;
+            for (int r = 0; r < n_cl; ++r) M = fmaxf(M, cl.map_shared_rank(merged, r)[H * DH + head]);
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < n_cl; ++r) {
+                const float *rp = cl.map_shared_rank(merged, r);
+                const float m = rp[H * DH + head], rl = rp[H * DH + H + head];
+                if (m == -INFINITY && rl == 0.f) continue;
+                const float w = exp2f(m - M);
+                const float4 v = reinterpret_cast<const float4 *>(rp)[i4];
+                l += w * rl;
+                acc.x += w * v.x;
+                acc.y += w * v.y;
+                acc.z += w * v.z;
+                acc.w += w * v.w;
+            }
+            const float f = l == 0.f ? 0.f : a.p.out_scale / l;
+            __nv_bfloat162 w2[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
+            *reinterpret_cast<uint2 *>(a.p.out + (size_t)b * H * DH + i4 * 4) = *reinterpret_cast<const uint2 *>(w2);
+        }
+        cl.sync();                                         // peers read this CTA's shared memory
+    };
+    auto empty_partial = [&] {
+        for (int i = tid; i < H; i += C::THREADS) {
+            if (a.cluster) {
+                merged[H * DH + i] = -INFINITY;
+                merged[H * DH + H + i] = 0.f;
+            } else {
+                *reinterpret_cast<float2 *>(a.p.part_ml + ((size_t)(b * H + i) * a.p.n_split + split) * 2) =
+                    make_float2(-INFINITY, 0.f);
+            }
+        }
+        if (a.cluster) join_cluster();
+    };
     if (v0 >= v1) {                                        // nothing here: zeros, or an empty partial
         if (a.p.n_split == 1) {
             for (int i = tid; i < H * DH; i += C::THREADS)
                 a.p.out[(size_t)b * H * DH + i] = __float2bfloat16_rn(0.f);
         } else {
-            for (int i = tid; i < H; i += C::THREADS)
-                *reinterpret_cast<float2 *>(a.p.part_ml + ((size_t)(b * H + i) * a.p.n_split + split) * 2) =
-                    make_float2(-INFINITY, 0.f);
+            empty_partial();
         }
         return;
     }
@@ -644,6 +692,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             for (int t = max(0, n_tiles - STAGES); t < n_tiles; ++t)
                 (void)mbar_wait(full0 + 8 * (t % STAGES), (t / STAGES) & 1, a.limit_ns);
         __syncthreads();
+        if (a.p.n_split > 1) empty_partial();               // (the error is reported; peers must not wait)
         return;
     }
 
@@ -655,7 +704,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             l_run[mt][hr] += __shfl_xor_sync(0xffffffffu, l_run[mt][hr], 1);
             l_run[mt][hr] += __shfl_xor_sync(0xffffffffu, l_run[mt][hr], 2);
         }
-    float *mo = reinterpret_cast<float *>(smem), *mm = mo + SLICES * H * C::MO_LD;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -697,6 +745,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         if (a.p.n_split == 1) {
             __nv_bfloat162 w2[2] = {__floats2bfloat162_rn(acc.x, acc.y), __floats2bfloat162_rn(acc.z, acc.w)};
             *reinterpret_cast<uint2 *>(a.p.out + (size_t)b * H * DH + i4 * 4) = *reinterpret_cast<const uint2 *>(w2);
+        } else if (a.cluster) {
+            reinterpret_cast<float4 *>(merged)[i4] = acc;
+            if (col == 0) {
+                merged[H * DH + head] = M;
+                merged[H * DH + H + head] = l;
+            }
         } else {
             const size_t at = (size_t)(b * H + head) * a.p.n_split + split;
             *reinterpret_cast<float4 *>(a.p.part_o + at * DH + col) = acc;
@@ -705,6 +759,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     }
     // a cached value that is not finite, or an operand outside the fp16 range
     if (!finite) raise_error(a.p.err, kErrDeviceCheck);
+    if (a.cluster) join_cluster();
 }
 
 // (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools)
@@ -729,12 +784,42 @@ cudaError_t launch_cfg(const DecodeArgsP &a, cudaStream_t st) {
     lc.blockDim = dim3(C::THREADS);
     lc.dynamicSmemBytes = C::SMEM;
     lc.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster ? (unsigned)a.p.n_split : 1u;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, paged_decode_kernel<C>, a);
+}
+
+// Clusters of `size` CTAs that can be resident at once on the current device (0: none).
+template <class C>
+int max_clusters(int size) {
+    if (ensure_dynamic_smem<paged_decode_kernel<C>>(C::SMEM) != cudaSuccess) return 0;
+    if (size > 8 && cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                        cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)size);
+    lc.blockDim = dim3(C::THREADS);
+    lc.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, paged_decode_kernel<C>, a);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, paged_decode_kernel<C>, &lc) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 }  // namespace
@@ -772,12 +857,38 @@ void paged_decode_shape(int variant, bool e4m3, int *tile_groups, int *ctas_per_
     if (*ctas_per_sm < 1) *ctas_per_sm = 1;
 }
 
+int paged_decode_max_clusters(int variant, bool e4m3, int size) {
+    // asked once per device, variant, format and size
+    constexpr int kDevices = 64, kVariants = 10;
+    static std::atomic<int> known[kDevices][kVariants][2][kPagedMaxCluster + 1];
+    int dev = 0;
+    if (size < 2 || size > kPagedMaxCluster || variant < 0 || variant >= kVariants || cudaGetDevice(&dev) != cudaSuccess ||
+        dev < 0 || dev >= kDevices)
+        return 0;
+    std::atomic<int> &k = known[dev][variant][e4m3][size];
+    if (k.load() == 0) {
+        int n = 0;
+        switch (variant) {
+#define KPA_CLUSTERS(IDX, MA, D1, D2, RK, RV, H2, HS, S0, C0, T0, S1, C1, T1)                        \
+    case IDX:                                                                                        \
+        n = e4m3 ? max_clusters<Cfg<MA, D1, D2, RK, RV, H2, S1, HS, C1, T1, true>>(size)             \
+                 : max_clusters<Cfg<MA, D1, D2, RK, RV, H2, S0, HS, C0, T0, false>>(size);           \
+        break;
+            KPA_PAGED_DECODE_VARIANTS(KPA_CLUSTERS)
+#undef KPA_CLUSTERS
+        }
+        k.store(n > 0 ? n : -1);
+    }
+    return k.load() > 0 ? k.load() : 0;
+}
+
 cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &p, int groups_per_split,
-                                unsigned long long wait_limit_ns, cudaStream_t st) {
+                                bool cluster, unsigned long long wait_limit_ns, cudaStream_t st) {
     DecodeArgsP a;
     a.p = p;
     a.pool = s.pool;
     a.gps = groups_per_split;
+    a.cluster = cluster;
     a.limit_ns = wait_limit_ns;
     cudaError_t e = cudaErrorInvalidValue;
     switch (variant) {
@@ -789,7 +900,7 @@ cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAtt
         KPA_PAGED_DECODE_VARIANTS(KPA_CASE)
 #undef KPA_CASE
     }
-    if (e != cudaSuccess || p.n_split == 1) return e;
+    if (e != cudaSuccess || p.n_split == 1 || cluster) return e;
     return launch_paged_combine(s, p, st);
 }
 
