@@ -66,17 +66,16 @@ __device__ __forceinline__ bool find_group(const WriteArgs &a, Group &g) {
     return true;
 }
 
-// Where it lies in a pool plane, or null: reported.
-template <class Byte>
-__device__ __forceinline__ Byte *group_at(const WriteArgs &a, const Group &g, Byte *plane, int bytes) {
+// Which group of the pool it is, or -1: reported.
+__device__ __forceinline__ long long pool_group(const WriteArgs &a, const Group &g) {
     if (g.slot0 >= 0 && g.slot0 + 16 <= a.max_slots) {          // (the table's range is whole groups)
         int entry, in;
         split_group(a.pool, (int)(g.slot0 >> 4), entry, in);
         const int page = __ldg(a.pool.table + (size_t)g.b * a.pool.table_stride + entry);
-        if (page >= 0 && page < a.pool.n_pages) return plane + ((size_t)page * a.pool.pg + in) * (size_t)bytes;
+        if (page >= 0 && page < a.pool.n_pages) return (long long)page * a.pool.pg + in;
     }
     if (threadIdx.x == 0) raise_error(a.err, kErrDeviceCheck);
-    return nullptr;
+    return -1;
 }
 
 __device__ __forceinline__ float finite_abs(float x) {
@@ -149,8 +148,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) paged_append_kernel(WriteArgs 
         }
     };
     load(tid);                                    // in flight while the table entry and the angles are
-    unsigned char *const dst0 = group_at(a, g, is_k ? a.kpool : a.vpool, is_k ? a.pool.kg : a.pool.vg);
-    if (!dst0) return;
+    const long long at = pool_group(a, g);
+    if (at < 0) return;
+    unsigned char *const dst0 = is_k ? a.kpool + (size_t)at * a.pool.kg : a.vpool + (size_t)at * a.pool.vg;
     if (is_k) {
         for (int i = tid; i < 16 * half; i += threads) {
             const int t = i & 15;
@@ -257,63 +257,71 @@ __global__ void __launch_bounds__(kMaxThreads, 2) paged_append_kernel(WriteArgs 
     }
 }
 
-// VEC: records start on 4-byte boundaries.
+// VEC: records start on 4-byte boundaries.  One CTA takes a group's keys and values, whose loads
+// are in flight together.
 template <bool E4M3, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 2) paged_read_kernel(WriteArgs a) {
-    const bool is_k = blockIdx.y == 0;
-    const int E = is_k ? a.ek : a.ev, A = is_k ? a.ak : a.av;
     Group g;
     if (!find_group(a, g)) return;
-    const unsigned char *const from = group_at(a, g, is_k ? a.pool.k : a.pool.v, is_k ? a.pool.kg : a.pool.vg);
+    const long long at = pool_group(a, g);
     const int tid = threadIdx.x, threads = blockDim.x;
-    __nv_bfloat16 *rec = (is_k ? a.kf : a.vf) + (size_t)g.row0 * E - (size_t)g.t0 * E;
-    uint32_t sa[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
-    if (E4M3 && from) {
-        const uint4 u = reinterpret_cast<const uint4 *>(from)[E], v = reinterpret_cast<const uint4 *>(from)[E + 1];
-        sa[0] = u.x, sa[1] = u.y, sa[2] = u.z, sa[3] = u.w;
-        sb[0] = v.x, sb[1] = v.y, sb[2] = v.z, sb[3] = v.w;
-    }
-    for (int e = 2 * tid; e < E; e += 2 * threads) {
-        const bool one = e + 1 >= E;
-        // the two elements at slots k and k + 8 as fp32 (a page outside the pool: zeros)
-        uint32_t w[16];
+    constexpr int N = E4M3 ? 1 : 2;               // 16-byte vectors of an element's 16 slots
+    struct Plane {
+        const uint4 *rows;                        // the group's, or null (zeros are read)
+        int E, A;
+        __nv_bfloat16 *rec;                       // of slot 0 of the group
+    };
+    auto plane = [&](bool is_k) {
+        Plane p;
+        p.E = is_k ? a.ek : a.ev;
+        p.A = is_k ? a.ak : a.av;
+        p.rows = at < 0 ? nullptr
+                        : reinterpret_cast<const uint4 *>(is_k ? a.pool.k + (size_t)at * a.pool.kg : a.pool.v + (size_t)at * a.pool.vg);
+        p.rec = (is_k ? a.kf : a.vf) + ((long long)g.row0 - g.t0) * p.E;
+        return p;
+    };
+    // elements e, e + 1 (the last of an odd record has no second) and the scale row of e's part
+    auto load = [&](const Plane &p, int e, uint4 (&x)[2][N], uint4 &scale) {
+        if (E4M3) scale = p.rows && e < p.E ? __ldg(p.rows + p.E + (e < p.A ? 0 : 1)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int t = 0; t < 16; ++t) w[t] = 0u;
-        if (from) {
-            if constexpr (E4M3) {
-                const uint4 *row = reinterpret_cast<const uint4 *>(from) + e;
-                const uint4 u = row[0], v = one ? u : row[1];
-                const uint32_t c0[4] = {u.x, u.y, u.z, u.w}, c1[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 x0 = h2_to_f2(e4m3x2_to_h2(c0[k >> 1] >> (16 * (k & 1))));
-                    const float2 x1 = h2_to_f2(e4m3x2_to_h2(c1[k >> 1] >> (16 * (k & 1))));
-                    const uint32_t s0 = (e < A ? sa : sb)[k >> 1] >> (16 * (k & 1)),
-                                   s1 = (e + 1 < A ? sa : sb)[k >> 1] >> (16 * (k & 1));
+            for (int n = 0; n < N; ++n)
+                x[i][n] = p.rows && e + i < p.E ? __ldg(p.rows + (size_t)n * p.E + e + i) : make_uint4(0, 0, 0, 0);
+    };
+    auto emit = [&](const Plane &p, int e, const uint4 (&x)[2][N], const uint4 s0) {
+        if (e >= p.E) return;
+        uint32_t w[16];                           // the pair at each slot
+        if constexpr (E4M3) {
+            const uint4 s1 = p.rows && e + 1 == p.A ? __ldg(p.rows + p.E + 1) : s0;      // (an odd A ends between them)
+            const uint32_t c0[4] = {x[0][0].x, x[0][0].y, x[0][0].z, x[0][0].w}, c1[4] = {x[1][0].x, x[1][0].y, x[1][0].z, x[1][0].w};
+            const uint32_t e0[4] = {s0.x, s0.y, s0.z, s0.w}, e1[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-                    for (int u2 = 0; u2 < 2; ++u2) {
-                        const float y0 = (u2 ? x0.y : x0.x) * exp_byte((s0 >> (8 * u2)) & 255u);
-                        const float y1 = (u2 ? x1.y : x1.x) * exp_byte((s1 >> (8 * u2)) & 255u);
-                        // exact in bf16: four significant bits
-                        w[k + 8 * u2] = (__float_as_uint(y0) >> 16) | (__float_as_uint(y1) & 0xffff0000u);
-                    }
-                }
-            } else {
+            for (int k = 0; k < 8; ++k) {         // slots k and k + 8
+                const int sh = 16 * (k & 1);
+                const float2 x0 = h2_to_f2(e4m3x2_to_h2(c0[k >> 1] >> sh)), x1 = h2_to_f2(e4m3x2_to_h2(c1[k >> 1] >> sh));
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint4 *row = reinterpret_cast<const uint4 *>(from) + (size_t)hf * E + e;
-                    const uint4 u = row[0], v = one ? u : row[1];
-                    const uint32_t c0[4] = {u.x, u.y, u.z, u.w}, c1[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w[8 * hf + k] = __byte_perm(c0[k >> 1], c1[k >> 1], k & 1 ? 0x7632 : 0x5410);
+                for (int u = 0; u < 2; ++u) {
+                    const float y0 = (u ? x0.y : x0.x) * exp_byte((e0[k >> 1] >> (sh + 8 * u)) & 255u);
+                    const float y1 = (u ? x1.y : x1.x) * exp_byte((e1[k >> 1] >> (sh + 8 * u)) & 255u);
+                    // exact in bf16: four significant bits
+                    w[k + 8 * u] = (__float_as_uint(y0) >> 16) | (__float_as_uint(y1) & 0xffff0000u);
                 }
             }
+        } else {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint4 u = x[0][hf * (N - 1)], v = x[1][hf * (N - 1)];
+                const uint32_t c0[4] = {u.x, u.y, u.z, u.w}, c1[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[8 * hf + k] = __byte_perm(c0[k >> 1], c1[k >> 1], k & 1 ? 0x7632 : 0x5410);
+            }
         }
+        const bool one = e + 1 >= p.E;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             if (t < g.t0 || t >= g.t1) continue;
-            __nv_bfloat16 *r = rec + (size_t)t * E + e;
+            __nv_bfloat16 *r = p.rec + (long long)t * p.E + e;
             if (VEC) {
                 *reinterpret_cast<uint32_t *>(r) = w[t];
             } else {
@@ -321,6 +329,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) paged_read_kernel(WriteArgs a)
                 if (!one) r[1] = __ushort_as_bfloat16((unsigned short)(w[t] >> 16));
             }
         }
+    };
+    const Plane k = plane(true), v = plane(false);
+    for (int e = 2 * tid; e < max(k.E, v.E); e += 2 * threads) {
+        uint4 xk[2][N], xv[2][N], sk, sv;
+        load(k, e, xk, sk);
+        load(v, e, xv, sv);
+        emit(k, e, xk, sk);
+        emit(v, e, xv, sv);
     }
 }
 
@@ -358,9 +374,7 @@ void by_format(bool e4m3, bool vec, Launch launch) {
 }
 
 // n rows of one sequence touch at most (n + 14) / 16 + 1 groups
-dim3 write_grid(int batch, int n_rows) {
-    return dim3((unsigned)(((long long)n_rows + 14ll * batch) / 16 + batch), 2);
-}
+unsigned write_groups(int batch, int n_rows) { return (unsigned)(((long long)n_rows + 14ll * batch) / 16 + batch); }
 
 }  // namespace
 
@@ -372,7 +386,7 @@ cudaError_t launch_paged_append(const PagedShape &s, int batch, int n_rows, cons
     a.vf = const_cast<__nv_bfloat16 *>(static_cast<const __nv_bfloat16 *>(vf));
     a.kpool = static_cast<unsigned char *>(kpool);
     a.vpool = static_cast<unsigned char *>(vpool);
-    const dim3 grid = write_grid(batch, n_rows);
+    const dim3 grid(write_groups(batch, n_rows), 2);                    // (y: the plane)
     const bool vec = a.ek % 2 == 0 && a.ev % 2 == 0 && a.ak % 2 == 0 && a.av % 2 == 0;
     const size_t smem = (size_t)(a.d2 / 2) * 16 * sizeof(float2);       // at most 16 KB
     by_format(s.pool.e4m3 != 0, vec, [&](auto e4m3, auto v) {
@@ -386,7 +400,7 @@ cudaError_t launch_paged_read(const PagedShape &s, int batch, int n_rows, const 
     WriteArgs a = write_args(s, batch, n_rows, cu, start, err);
     a.kf = static_cast<__nv_bfloat16 *>(kf);
     a.vf = static_cast<__nv_bfloat16 *>(vf);
-    const dim3 grid = write_grid(batch, n_rows);
+    const unsigned grid = write_groups(batch, n_rows);
     by_format(s.pool.e4m3 != 0, a.ek % 2 == 0 && a.ev % 2 == 0, [&](auto e4m3, auto v) {
         paged_read_kernel<decltype(e4m3)::value, decltype(v)::value><<<grid, threads_of(a), 0, st>>>(a);
     });
