@@ -97,6 +97,29 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return r;
 }
 
+// Low word of a shared-memory descriptor (umma_desc_k_sw128's address and leading offset); the
+// high word is the same for every tile.
+__device__ __forceinline__ uint32_t umma_lo(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3FFFu) | (1u << 16); }
+constexpr uint32_t kUmmaHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A B^T with A in shared memory, or in tensor memory; issued by one thread.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kUmmaHi)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kUmmaHi)
+        : "memory");
+}
+
 // mbarrier slots
 enum : int {
     B_Q = 0,
@@ -348,18 +371,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
                 if (ok && tp.act[hh] && !wait(B_QREADY + hh, 0)) ok = false;
+            const uint32_t d_q = umma_lo(smem_u32(smem + C::OFF_Q)), d_k = umma_lo(smem_u32(smem + C::OFF_K)),
+                           d_v = umma_lo(smem_u32(smem + C::OFF_V));
             auto issue_s = [&](int hh, int t) -> bool {
                 const int kb = t & 1;
                 if (!wait(B_K_FULL + kb, (t >> 1) & 1)) return false;
                 tc_fence_after();
+            const uint32_t q_lo = d_q + hh * (C::Q_HALF >> 4), k_lo = d_k + kb * (C::KV_TILE >> 4), s_addr = tmem + hh * 128;
 #pragma unroll
-                for (int k = 0; k < DH / 16; ++k) {
-                    const uint64_t qd =
-                        umma_desc_k_sw128(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + (k / 4) * HQ * 128)) + 2 * (k % 4);
-                    const uint64_t kd =
-                        umma_desc_k_sw128(smem_u32(smem + C::OFF_K + kb * C::KV_TILE + (k / 4) * TK * 128)) + 2 * (k % 4);
-                    umma_bf16(tmem + hh * 128, qd, kd, idesc_s, k > 0);
-                }
+            for (int k = 0; k < DH / 16; ++k)
+                umma_ss(s_addr, q_lo + (k / 4) * (HQ * 128 >> 4) + 2 * (k % 4), k_lo + (k / 4) * (TK * 128 >> 4) + 2 * (k % 4),
+                        idesc_s, k > 0);
                 umma_commit(bar(B_S_FULL + hh));
                 if (hh == tp.last_half(t)) umma_commit(bar(B_K_EMPTY + kb));
                 return true;
@@ -374,9 +396,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                         if (!wait(B_P_FULL + hh, t & 1)) return false;
                         tc_fence_after();
                     }
-                    const uint64_t vd =
-                        umma_desc_k_sw128(smem_u32(smem + C::OFF_V + (k / 4) * DH * 128)) + 2 * (k % 4);
-                    umma_ts(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, vd, idesc_o, t > 0 || k > 0);
+                    umma_ts_lo(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, d_v + (k / 4) * (DH * 128 >> 4) + 2 * (k % 4), idesc_o, t > 0 || k > 0);
                 }
                 if (hh == tp.last_half(t)) umma_commit(bar(B_V_EMPTY));
                 if (t == tp.last[hh]) umma_commit(bar(B_O_FINAL + hh));
