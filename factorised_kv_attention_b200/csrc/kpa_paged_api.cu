@@ -122,22 +122,23 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
     return p;
 }
 
-kpa_status check_attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32_t n_rows, int32_t max_len,
-                      int32_t window, int32_t sinks, PagedShape *s) {
+kpa_status check_attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32_t n_rows, bool chunks,
+                      int32_t max_len, int32_t window, int32_t sinks, PagedShape *s) {
     kpa_status st = check_paged(cfg, pg, s);
     if (st != KPA_OK && st != KPA_ERR_UNSUPPORTED) return st;
     if (batch < 0 || n_rows < 0 || max_len < 0 || window < 0 || sinks < 0) return KPA_ERR_INVALID_ARG;
     if ((int64_t)max_len > (int64_t)pg->page_size * pg->table_stride) return KPA_ERR_INVALID_ARG;
     if (st != KPA_OK) return st;
     if (!paged_mma_supported(s->d, s->pool.e4m3 != 0)) return KPA_ERR_UNSUPPORTED;
-    if (n_rows > INT32_MAX / 2 || batch > 65535) return KPA_ERR_UNSUPPORTED;
+    // row tiles (of chunks) and sequences (single tokens) are blocks in y
+    if (batch > 65535 || (chunks && n_rows / paged_mma_rows() + (int64_t)batch > 65535)) return KPA_ERR_UNSUPPORTED;
     return KPA_OK;
 }
 
 kpa_status workspace_size(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32_t n_rows, bool chunks,
                           int32_t max_len, int32_t window, int32_t sinks, size_t *bytes) {
     PagedShape s;
-    kpa_status st = check_attn(cfg, pg, batch, n_rows, max_len, window, sinks, &s);
+    kpa_status st = check_attn(cfg, pg, batch, n_rows, chunks, max_len, window, sinks, &s);
     if (st != KPA_OK) return st;
     if (!bytes) return KPA_ERR_INVALID_ARG;
     *bytes = 0;
@@ -155,7 +156,7 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
                 const void *kpool, const void *vpool, int32_t max_len, int32_t window, int32_t sinks, float sm_scale,
                 void *out, void *workspace, size_t ws_bytes, kpa_stream stream) {
     PagedShape s;
-    kpa_status st = check_attn(cfg, pg, batch, n_rows, max_len, window, sinks, &s);
+    kpa_status st = check_attn(cfg, pg, batch, n_rows, chunks, max_len, window, sinks, &s);
     if (st != KPA_OK && st != KPA_ERR_UNSUPPORTED) return st;
     if (!isfinite(sm_scale)) return KPA_ERR_INVALID_ARG;
     if (st != KPA_OK) return st;
@@ -168,8 +169,6 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
     st = device_info(&err, &sms);
     if (st != KPA_OK) return st;
     const AttnPlan p = plan_attn(s, batch, n_rows, chunks, max_len, window, sinks, sms);
-    // row tiles are blocks in y
-    if (chunks && n_rows / paged_mma_rows() + (int64_t)batch > 65535) return KPA_ERR_UNSUPPORTED;
     if (p.bytes > 0) {
         if (!workspace || ws_bytes < p.bytes) return KPA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return KPA_ERR_INVALID_ARG;

@@ -552,9 +552,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                 if constexpr (Q8) {
                     const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * (KG + VG) + KG + C::EV * 16 + 4 * c;
                     const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
-                    // 2^8 times the scales
-                    vs[0] = pack_h2(256.f * exp_sum(s4 & 255u), 256.f * exp_sum((s4 >> 16) & 255u));
-                    vs[1] = pack_h2(256.f * exp_sum((s4 >> 8) & 255u), 256.f * exp_sum(s4 >> 24));
+                    // 2^8 times the scales go to B; what would take B below 2^-16 goes to the weights instead
+                    // (values near 2^-30 and less: rarely, and for the whole warp at once)
+                    float2 f[2] = {make_float2(256.f * exp_sum(s4 & 255u), 256.f * exp_sum((s4 >> 16) & 255u)),
+                                   make_float2(256.f * exp_sum((s4 >> 8) & 255u), 256.f * exp_sum(s4 >> 24))};
+                    constexpr float kLow = 1.f / 65536.f;
+                    if (__any_sync(0xffffffffu, fminf(fminf(f[0].x, f[0].y), fminf(f[1].x, f[1].y)) < kLow)) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const float2 w = make_float2(fminf(1.f, f[hf].x * 65536.f), fminf(1.f, f[hf].y * 65536.f));
+                            f[hf] = make_float2(fmaxf(f[hf].x, kLow), fmaxf(f[hf].y, kLow));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int hr = 0; hr < HR; ++hr) sc[cc][mt][hr][hf] = fmul2(sc[cc][mt][hr][hf], w);
+                        }
+                    }
+                    vs[0] = pack_h2(f[0].x, f[0].y);
+                    vs[1] = pack_h2(f[1].x, f[1].y);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

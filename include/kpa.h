@@ -357,12 +357,14 @@ kpa_status kpa_append(const kpa_config *cfg, int32_t batch, int32_t n_tok, const
  * int32, ascending), row cu_rows[b] + t at position start_pos[b] + t.  A sequence may have
  * no rows.  Rows of no sequence (before cu_rows[0], or at and behind cu_rows[batch]) are
  * neither read nor written.  A sequence whose cu_rows descend or leave [0, n_rows] sets
- * KPA_ERR_DEVICE_CHECK and is skipped.
+ * KPA_ERR_DEVICE_CHECK and is skipped (an attention may leave unspecified values in the
+ * rows of `out` that it names).
  *
  * Page table entries are looked at only for slots that the call writes or that some of its
  * rows see; the others may hold anything.  An entry outside [0, n_pages) sets
  * KPA_ERR_DEVICE_CHECK: nothing is written to it, a read returns zeros for it, and the
- * attention of the rows that see it is unspecified. */
+ * attention of the rows that see it is unspecified.  Sequences may share pages that no
+ * call in flight writes (a common prefix). */
 typedef enum { KPA_PAGE_BF16 = 0, KPA_PAGE_E4M3 = 1 } kpa_page_format;
 
 typedef struct {
@@ -405,13 +407,17 @@ kpa_status kpa_paged_read_factors(const kpa_config *cfg, const kpa_pages *pages,
  *        or above it, or below 0, gets zeros and sets KPA_ERR_DEVICE_CHECK
  *   window >= 0, sinks >= 0
  *   workspace at least kpa_paged_prefill_workspace_size bytes, 256-byte aligned; it needs
- *        no initialisation and holds nothing between calls
- * K and V are rebuilt from the factors on chip and rounded once to fp16; products
- * accumulate in fp32, and the softmax is fp32.  A cached value that is not finite, or a
- * rebuilt one outside fp16's range, makes the rows that see it, and possibly other rows of
- * the same sequence and call, non-finite and sets KPA_ERR_DEVICE_CHECK; slots that none of
- * the sequence's rows sees, whatever they hold, change nothing.
- * Takes every split with d_h <= 128 that kpa_prefill takes.  Results are deterministic. */
+ *        no initialisation and holds nothing between calls.  Calls that may run at the same
+ *        time need workspaces of their own.
+ * K and V are rebuilt from the factors on chip and rounded once to fp16, as are the scaled
+ * query and the softmax weights; products accumulate in fp32, and the softmax is fp32.  A
+ * cached value that is not finite, or a rebuilt one outside fp16's range, leaves the rows
+ * that see it, and possibly other rows of the same sequence and call, unspecified; outputs
+ * that are not finite set KPA_ERR_DEVICE_CHECK.  Slots that none of the sequence's rows
+ * sees, whatever they hold, change nothing.
+ * Takes the splits with d_h <= 128 whose slices fit the kernel's staging (as kpa_prefill),
+ * and n_rows / 128 + batch up to 65535; KPA_ERR_UNSUPPORTED otherwise.  Results are
+ * deterministic. */
 kpa_status kpa_paged_prefill_workspace_size(const kpa_config *cfg, const kpa_pages *pages, int32_t batch,
                                             int32_t n_rows, int32_t max_len, int32_t window, int32_t sinks,
                                             size_t *bytes);
@@ -429,7 +435,7 @@ kpa_status kpa_paged_prefill(const kpa_config *cfg, const kpa_pages *pages, int3
  *   seq_len [batch] int32  0 <= seq_len[b] <= max_len; a longer length is clamped to
  *        max_len, a negative one to 0, and sets KPA_ERR_DEVICE_CHECK; 0 gives zeros
  *   out  [batch][h][d_h]  bf16
- * Other rules as kpa_paged_prefill. */
+ * batch up to 65535.  Other rules as kpa_paged_prefill. */
 kpa_status kpa_paged_decode_workspace_size(const kpa_config *cfg, const kpa_pages *pages, int32_t batch,
                                            int32_t max_len, int32_t window, int32_t sinks, size_t *bytes);
 kpa_status kpa_paged_decode(const kpa_config *cfg, const kpa_pages *pages, int32_t batch, const void *q,

@@ -250,7 +250,7 @@ def test_prefill(name, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "kpa_4x8_8x16_r4", "kpa_4x4_8x8_r2", "tpa_16_128_r2", "kpa_3x2_4x6_r2"])
+@pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "kpa_4x8_8x16_r4", "kpa_4x4_8x8_r2", "tpa_16_128_r2", "tpa_32_64_r1", "kpa_3x2_4x6_r2"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (100, 70), (130, 1), (5000, 9), (64, 1000)])
 def test_prefill_window(name, fmt, window, sinks):
     _prefill(kpa(), SPLITS[name], fmt, 48, [0, 290, 701, 64], [140, 130, 3, 260], window, sinks, 11)
@@ -288,6 +288,136 @@ def test_decode_long(name, fmt):
 def test_decode_large_batch(fmt):
     rng = np.random.default_rng(24)
     _decode(kpa(), SPLITS["kpa_4x4_8x16_r2"], fmt, 16, [int(x) for x in rng.integers(0, 200, 333)], 90, 2, 24)
+
+
+@pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "tpa_16_64_r2", "kpa_3x2_4x6_r2"])
+def test_prefill_many_sequences(name):
+    """More sequences than the ordered search of a row tile holds."""
+    rng = np.random.default_rng(25)
+    past, new = [int(x) for x in rng.integers(0, 60, 300)], [int(x) for x in rng.integers(0, 4, 300)]
+    new[7], new[250] = 300, 131
+    _prefill(kpa(), SPLITS[name], "e4m3", 16, past, new, 40, 3, 25)
+
+
+def test_every_kernel_is_reached():
+    """The splits of these tests reach each kernel of both attentions."""
+    lib = kpa()
+    pages = lib.make_pages(16, 10, 10)
+    kinds = {n: (lib.kpa_paged_decode_kernel_kind(lib.make_config(s, "bf16"), pages),
+                 lib.kpa_paged_prefill_kernel_kind(lib.make_config(s, "bf16"), pages)) for n, s in SPLITS.items()}
+    assert kinds["kpa_3x2_4x6_r2"] == kinds["kpa_4x4_8x16_rk3_rv1"] == ("chunks", "chunks")
+    assert kinds["tpa_61_64_r1"] == ("chunks", "tcgen05")
+    assert all(kinds[n] == ("factors", "tcgen05") for n in NAMES if n not in
+               ("kpa_3x2_4x6_r2", "kpa_4x4_8x16_rk3_rv1", "tpa_61_64_r1"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "tpa_16_64_r2", "kpa_3x2_4x6_r2"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_other_scales(name, fmt, scale):
+    """No scale, a negative one, and one that leaves a softmax of few tokens."""
+    lib = kpa()
+    s = SPLITS[name]
+    c = pu.Cache(s, fmt, 16, [90, 33], 70)
+    cfg, pages = lib.make_config(s, "bf16"), c.descriptor(lib)
+    q = _q(np.random.default_rng(71), 2, s)
+    t, k, v = c.table.cuda(), c.k.cuda(), c.v.cuda()
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+    for decode in (True, False):
+        if decode:
+            lib.kpa_paged_decode(cfg, pages, 2, q.cuda(), _i32([90, 33]), t, k, v, 90, 0, 0, scale, out, ws)
+        else:
+            lib.kpa_paged_prefill(cfg, pages, 2, 2, q.cuda(), _i32([0, 1, 2]), _i32([89, 32]), t, k, v, 90, 0, 0, scale, out, ws)
+        _no_error(lib)
+        for b, n in enumerate((90, 33)):
+            want, tol = pu.attention(c, b, pu.f64(q[b:b + 1]), [n - 1], 0, 0, scale, factored=decode)
+            pu.assert_within(out[b:b + 1], want, tol, f"sequence {b}, decode {decode}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_values_of_many_magnitudes(fmt):
+    """Tokens whose factors differ by powers of two up to 2^12, and tiny ones throughout."""
+    lib = kpa()
+    s = SPLITS["kpa_4x8_8x16_r2"]
+    for level in (0, -10):
+        c = pu.Cache(s, fmt, 32, [0, 0], 72, spare=8, stride=4)
+        rng = np.random.default_rng(73)
+        c.table[:, :4] = torch.arange(8, dtype=torch.int32).view(2, 4)
+        for plane, pool, e in ((c.kp, c.k, s.e_k), (c.vp, c.v, s.e_v)):
+            x = rng.standard_normal((256, e)) * np.exp2(rng.integers(-6, 7, (256, 1)) / 2 + level)
+            plane.write(pool, np.arange(256) // 32, np.arange(256) % 32, x)
+        cfg, pages = lib.make_config(s, "bf16"), c.descriptor(lib)
+        q = _q(rng, 2, s)
+        ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+        out = torch.empty(2, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+        args = (c.table.cuda(), c.k.cuda(), c.v.cuda(), 128, 0, 0, 0.05, out, ws)
+        for decode in (True, False):
+            if decode:
+                lib.kpa_paged_decode(cfg, pages, 2, q.cuda(), _i32([128, 117]), *args)
+            else:
+                lib.kpa_paged_prefill(cfg, pages, 2, 2, q.cuda(), _i32([0, 1, 2]), _i32([127, 116]), *args)
+            _no_error(lib)
+            for b, n in enumerate((128, 117)):
+                want, tol = pu.attention(c, b, pu.f64(q[b:b + 1]), [n - 1], 0, 0, 0.05, factored=decode)
+                pu.assert_within(out[b:b + 1], want, tol, f"level {level}, sequence {b}, decode {decode}")
+
+
+def test_shared_pages():
+    """Two sequences that share the pages of a common prefix."""
+    lib = kpa()
+    s = SPLITS["kpa_4x4_8x16_r2"]
+    c = pu.Cache(s, "e4m3", 16, [64, 60], 74)
+    c.table[1, :2] = c.table[0, :2]
+    cfg, pages, scale = lib.make_config(s, "bf16"), c.descriptor(lib), 1.0 / np.sqrt(s.dh)
+    q = _q(np.random.default_rng(75), 12, s)
+    out = torch.empty(12, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    lib.kpa_paged_prefill(cfg, pages, 2, 12, q.cuda(), _i32([0, 4, 12]), _i32([60, 52]), c.table.cuda(), c.k.cuda(), c.v.cuda(),
+                          64, 0, 0, scale, out, ws)
+    _no_error(lib)
+    for b, (lo, hi, p) in enumerate(((0, 4, 60), (4, 12, 52))):
+        want, tol = pu.attention(c, b, pu.f64(q[lo:hi]), p + np.arange(hi - lo), 0, 0, scale)
+        pu.assert_within(out[lo:hi], want, tol)
+
+
+@pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "tpa_16_64_r2", "kpa_3x2_4x6_r2"])
+def test_positions_near_the_end_of_the_range(name):
+    """Slots just below 2^31, reached through a window."""
+    lib = kpa()
+    s = SPLITS[name]
+    page, stride = 4096, (1 << 19) - 1
+    cfg, pages = lib.make_config(s, "bf16"), lib.make_pages(page, 3, stride, "e4m3")
+    last = page * stride
+    n, window = 70, 50
+    start = last - n
+    kb, vb = lib.kpa_paged_page_bytes(cfg, pages)
+    k, v = (torch.full((3 * b,), 255, dtype=torch.uint8, device="cuda") for b in (kb, vb))
+    table = torch.full((1, stride), -1, **I32)
+    table[0, -1] = 1
+    rng = np.random.default_rng(76)
+    kf, vf = (torch.from_numpy(rng.standard_normal((n, e)) * 0.7).to(torch.bfloat16).cuda() for e in (s.e_k, s.e_v))
+    lib.kpa_paged_append_factors(cfg, pages, 1, n, kf, vf, _i32([0, n]), _i32([start]), table, k, v)
+    rk, rv = torch.empty_like(kf), torch.empty_like(vf)
+    lib.kpa_paged_read_factors(cfg, pages, 1, n, _i32([0, n]), _i32([start]), table, k, v, rk, rv)
+    _no_error(lib)
+    want = pu.rotate(pu.f64(kf), s, start + np.arange(n))
+    assert np.abs(pu.f64(rk) - want).max() <= 2.0 ** -4 * np.abs(want).max()
+    c = pu.Cache(s, "e4m3", page, [0], 0, stride=2)
+    c.records = lambda b, slots, *_: (pu.f64(rk)[slots], pu.f64(rv)[slots])
+    rows, scale = 15, 1.0 / np.sqrt(s.dh)
+    q = _q(rng, rows, s)
+    out = torch.empty(rows, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    lib.kpa_paged_prefill(cfg, pages, 1, rows, q.cuda(), _i32([0, rows]), _i32([last - rows]), table, k, v, last, window, 0, scale,
+                          out, ws)
+    _no_error(lib)
+    want, tol = pu.attention(c, 0, pu.f64(q), n - rows + np.arange(rows), window, 0, scale)
+    pu.assert_within(out, want, tol, "prefill")
+    lib.kpa_paged_decode(cfg, pages, 1, q[:1].cuda(), _i32([last]), table, k, v, last, window, 0, scale, out, ws)
+    _no_error(lib)
+    want, tol = pu.attention(c, 0, pu.f64(q[:1]), [n - 1], window, 0, scale, factored=True)
+    pu.assert_within(out[:1], want, tol, "decode")
 
 
 # ------------------------------------------------------------------ together
@@ -525,6 +655,32 @@ def test_other_stream_and_graph(fmt):
         _no_error(lib)
         for a, b in zip(got, outs):
             assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace and output."""
+    lib = kpa()
+    s = SPLITS["tpa_16_64_r2"]
+    c = pu.Cache(s, "bf16", 64, [5000, 4000], 52)
+    cfg, pages, scale = lib.make_config(s, "bf16"), c.descriptor(lib), 1.0 / np.sqrt(s.dh)
+    k, v, t = c.k.cuda(), c.v.cuda(), c.table.cuda()
+    q, cu, start, lens = _q(np.random.default_rng(53), 40, s).cuda(), _i32([0, 20, 40]), _i32([4980, 3980]), _i32([5000, 4000])
+    runs = []
+    for i in range(2):
+        out = torch.empty(40, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+        od = torch.empty(2, s.h, s.dh, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(max(256, lib.kpa_paged_prefill_workspace_size(cfg, pages, 2, 40, 5000),
+                             lib.kpa_paged_decode_workspace_size(cfg, pages, 2, 5000)), dtype=torch.uint8, device="cuda")
+        runs.append((torch.cuda.Stream(), out, od, ws))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for stream, out, od, ws in runs:
+            lib.kpa_paged_prefill(cfg, pages, 2, 40, q, cu, start, t, k, v, 5000, 0, 0, scale, out, ws, stream=stream)
+            lib.kpa_paged_decode(cfg, pages, 2, q, lens, t, k, v, 5000, 0, 0, scale, od, ws, stream=stream)
+    _no_error(lib)
+    assert torch.equal(runs[0][1], runs[1][1]) and torch.equal(runs[0][2], runs[1][2])
+    want, tol = pu.attention(c, 0, pu.f64(q[19:20]), [4999], 0, 0, scale)
+    pu.assert_within(runs[0][1][19:20], want, tol)
 
 
 def test_far_page_offsets():
