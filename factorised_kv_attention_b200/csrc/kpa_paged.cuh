@@ -268,6 +268,8 @@ struct PagedAttnArgs {
     __nv_bfloat16 *out;
     float *part_o, *part_ml;      // n_split > 1: [n_rows][h][n_split][d_h] and [n_rows][h][n_split][2]
     int n_split;
+    int2 *slots;                  // splits sized on the device: (first slot, slots) of each sequence, and the
+                                  // partials are [slot][h][d_h] and [slot][h][2]; else null
     int *err;
 };
 
@@ -288,7 +290,10 @@ int paged_decode_variant(const Dims &d);
 void paged_decode_shape(int variant, bool e4m3, int *tile_groups, int *ctas_per_sm);
 constexpr int kPagedMaxCluster = 16;
 int paged_decode_max_clusters(int variant, bool e4m3, int size);     // resident at once (at least 2 CTAs each)
+// groups_per_split: of a grid of n_split x batch blocks; with a.slots, n_slots blocks size the
+// splits themselves.
 cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &a, int groups_per_split,
-                                bool cluster, unsigned long long wait_limit_ns, cudaStream_t st);
+                                int n_slots, bool cluster, unsigned long long wait_limit_ns, cudaStream_t st);
+constexpr int kPagedMaxSlotSeqs = 256;                       // sequences that such a block can place
 
 }  // namespace kpa

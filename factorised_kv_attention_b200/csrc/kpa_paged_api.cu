@@ -46,18 +46,19 @@ struct AttnPlan {
     bool tcgen05;                // (chunk kernels) the tcgen05 one
     int groups_per_split;        // (single-token kernel)
     bool cluster;                // (single-token kernel) a sequence's splits merge in a cluster: no workspace
+    int n_slots;                 // (single-token kernel) blocks that size the splits themselves, or 0
     int n_split;
-    size_t ml_off, bytes;
+    size_t ml_off, slots_off, bytes;
 };
 
 // How the rows' key range is split.
 //  - The chunk kernels: with fewer CTAs than two per SM, into runs of at least four tiles
 //    (shorter ones cost more in partials than they gain), as many as make the last wave of
 //    CTAs end soonest when a CTA costs its tiles and three more.
-//  - The single-token kernel: one CTA per slot of the SMs for a single sequence; several
-//    sequences may have different lengths (the host does not see them), so up to four times
-//    as many shorter runs let the CTA scheduler even them out, as long as a run keeps eight
-//    tiles.
+//  - The single-token kernel: one CTA per slot of the SMs where that is one wave for the
+//    longest sequences there may be.  Where a batch would take more than that, or where its
+//    splits are long, the lengths decide, which the host does not see: the blocks of one wave
+//    (of up to four, to keep three splits a sequence) find the split size themselves.
 AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int max_len, int window, int sinks,
                    int sms) {
     const Dims &d = ps.d;
@@ -76,14 +77,17 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         const int64_t groups = std::max<int64_t>(1, visible(16, 1)), tiles = (groups + tg - 1) / tg;
         const int64_t per_seq = std::max<int64_t>(1, (int64_t)sms * per_sm / batch);
         int64_t per = (tiles + per_seq - 1) / per_seq;
-        if (batch > 1)
-            for (int k = 4; k > 1; --k) {
-                const int64_t t = (tiles + per_seq * k - 1) / (per_seq * k);
-                if (t >= 8) {
-                    per = t;
-                    break;
-                }
-            }
+        const int64_t wave = (int64_t)sms * per_sm;
+        if (batch > 1 && batch <= kPagedMaxSlotSeqs && (per >= 16 || per_seq == 1) && tiles >= 8) {
+            p.n_slots = (int)(wave * std::min<int64_t>(4, (3 * (int64_t)batch + wave - 1) / wave));
+            p.n_slots = std::max(p.n_slots, batch);
+            p.n_split = 2;                                 // (partials, in slots)
+            const size_t rh = (size_t)p.n_slots * d.h;
+            p.ml_off = (rh * d.dh * sizeof(float) + 255) & ~(size_t)255;
+            p.slots_off = p.ml_off + ((rh * 2 * sizeof(float) + 255) & ~(size_t)255);
+            p.bytes = p.slots_off + (((size_t)batch * sizeof(int2) + 255) & ~(size_t)255);
+            return p;
+        }
         // A sequence's splits merge in one cluster, without a second kernel, where every CTA is resident at
         // once (a cluster holds its SMs until its longest split ends) and the splits get no more than two
         // tiles or a quarter longer for it: the second kernel and its launch cost about as much.
@@ -193,9 +197,10 @@ kpa_status attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch, int32
     if (p.bytes > 0) {
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.ml_off);
+        if (p.n_slots > 0) a.slots = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + p.slots_off);
     }
     a.err = err;
-    const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split, p.cluster,
+    const cudaError_t e = p.variant >= 0 ? launch_paged_decode(p.variant, s, a, p.groups_per_split, p.n_slots, p.cluster,
                                                                device_wait_limit_ns(), (cudaStream_t)stream)
                           : p.tcgen05      ? launch_paged_prefill(s, a, device_wait_limit_ns(), (cudaStream_t)stream)
                                            : launch_paged_mma(s, a, (cudaStream_t)stream);

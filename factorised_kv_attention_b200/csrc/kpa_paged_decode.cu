@@ -48,7 +48,8 @@ using sm100::smem_u32;
 struct DecodeArgsP {
     PagedAttnArgs p;
     Pool pool;
-    int gps;                      // 16-slot groups per split
+    int gps;                      // 16-slot groups per split (the blocks find it, with p.slots)
+    int n_slots;                  // blocks, with p.slots
     int cluster;                  // the splits of a sequence are one cluster and merge over shared memory
     unsigned long long limit_ns;
 };
@@ -79,7 +80,7 @@ struct Cfg {
     static_assert(WARPS <= 16 && TG <= 32, "one warp issues a tile");
     static_assert((size_t)(SLICES * H * (MO_LD + 2) + H * (DH + 2)) * 4 <= (size_t)STAGES * STAGE_BYTES,
                   "slice merge and merged partial fit in the ring");
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(SMEM <= 226 * 1024, "shared memory (a little is static)");
 };
 
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t *r, std::integral_constant<int, 4>, std::false_type) {
@@ -154,7 +155,8 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t mask_pair(uint32_t v, bool k0, bool k1) {
     return (k0 ? (v & 0xffffu) : 0u) | (k1 ? (v & 0xffff0000u) : 0u);
 }
-template <class C>
+// SLOTS: the blocks size the splits themselves (a.p.slots).
+template <class C, bool SLOTS>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const DecodeArgsP a) {
     constexpr int MA = C::MA, D1 = C::D1, D2 = C::D2, RK = C::RK, RV = C::RV, H2 = C::H2, H = C::H, DH = C::DH;
     constexpr int MT = C::MT, HR = C::HR, NT = D2 / 8, KS = D2 == 8 ? 1 : D2 / 16;
@@ -166,7 +168,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     size_t *tab = reinterpret_cast<size_t *>(smem + C::OFF_TAB);
     volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.y, split = blockIdx.x;
     const int g = lane >> 2, c = lane & 3;
     const int i2 = warp % H2, hs = (warp / H2) % HS, slice = warp / (H2 * HS);
 
@@ -178,12 +179,75 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
+    // ---- splits sized here: the smallest number of tiles P per split with which all sequences' splits
+    // fit the blocks, so that one long sequence among short ones still loads every SM alike
+    __shared__ int place[3];                               // sequence, split, groups per split
+    if constexpr (SLOTS) {
+        if (warp == 0) {
+            constexpr int K = kPagedMaxSlotSeqs / 32;
+            int tiles[K], sum = 0, most = 1;               // of sequences lane + 32 k
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                tiles[k] = 0;
+                if (32 * k >= a.p.batch) continue;
+                const int s = lane + 32 * k;
+                const int n = s < a.p.batch ? min(a.p.seq_len[s], a.p.max_len) : 0;
+                tiles[k] = n > 0 ? (visible_tiles(a.p.mask, n - 1, n - 1, 16).n + TG - 1) / TG : 0;
+                sum += tiles[k];
+                most = max(most, tiles[k]);
+            }
+            sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+            most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+            const int blocks = (int)gridDim.x;             // (at least one per sequence)
+            int lo = max(1, sum / blocks), hi = most;      // hi does: one split per sequence
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                int n = 0;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (32 * k < a.p.batch) n += (int)((unsigned)(tiles[k] + mid - 1) / (unsigned)mid);
+                if ((int)__reduce_add_sync(0xffffffffu, (unsigned)n) <= blocks)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            // this block's sequence and split, in sequence order
+            int before = 0, mine = -1, first = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (32 * k >= a.p.batch) break;
+                const int n = (int)((unsigned)(tiles[k] + hi - 1) / (unsigned)hi);
+                int inc = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+                    if (lane >= off) inc += v;
+                }
+                const int at = before + inc - n;
+                if (blockIdx.x == 0 && lane + 32 * k < a.p.batch) a.p.slots[lane + 32 * k] = make_int2(at, n);
+                if ((int)blockIdx.x >= at && (int)blockIdx.x < at + n) mine = lane + 32 * k, first = at;
+                before += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) place[0] = -1;
+            __syncwarp();
+            if (mine >= 0) place[0] = mine, place[1] = (int)blockIdx.x - first, place[2] = hi * TG;
+            // (a bad length is reported by its first split's block; one without a split, here)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (blockIdx.x == 0 && lane + 32 * k < a.p.batch && a.p.seq_len[lane + 32 * k] < 0)
+                    raise_error(a.p.err, kErrDeviceCheck);
+        }
+        __syncthreads();
+        if (place[0] < 0) return;
+    }
+    const int b = SLOTS ? place[0] : (int)blockIdx.y, split = SLOTS ? place[1] : (int)blockIdx.x;
+    const int gps = SLOTS ? place[2] : a.gps;
     // ---- this CTA's groups: virtual groups v0 .. v1 - 1 of the sequence's visible ones
     const int32_t *trow = a.pool.table + (size_t)b * a.pool.table_stride;
     int len = a.p.seq_len[b];
     // without a window the first ring's table entries do not depend on the length: fetch them
     // beside it (inside the row for every slot below max_len)
-    const int v0 = split * a.gps;
+    const int v0 = split * gps;
     int first_page[C::FIRST], first_in[C::FIRST];
     const bool early = a.p.mask.window == 0;
 #pragma unroll
@@ -224,7 +288,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     Tiles tl = {0, 0, 0};
     if (len > 0) tl = visible_tiles(a.p.mask, pos, pos, 16);
     const int wstart = len > 0 ? window_start(a.p.mask, pos) : 0;
-    const int v1 = min(tl.n, v0 + a.gps);
+    const int v1 = min(tl.n, v0 + gps);
     float *mo = reinterpret_cast<float *>(smem), *mm = mo + SLICES * H * C::MO_LD;      // (after the loop)
     float *merged = mm + SLICES * H * 2;                   // [H][DH] o, [H] m, [H] l: this CTA's, for its cluster
     // the cluster's partials joined: each CTA a run of the outputs.  Every CTA of a cluster comes here.
@@ -257,14 +321,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         }
         cl.sync();                                         // peers read this CTA's shared memory
     };
+    auto partial_at = [&](int head) -> size_t {
+        return SLOTS ? (size_t)blockIdx.x * H + head : (size_t)(b * H + head) * a.p.n_split + split;
+    };
     auto empty_partial = [&] {
         for (int i = tid; i < H; i += C::THREADS) {
             if (a.cluster) {
                 merged[H * DH + i] = -INFINITY;
                 merged[H * DH + H + i] = 0.f;
             } else {
-                *reinterpret_cast<float2 *>(a.p.part_ml + ((size_t)(b * H + i) * a.p.n_split + split) * 2) =
-                    make_float2(-INFINITY, 0.f);
+                *reinterpret_cast<float2 *>(a.p.part_ml + partial_at(i) * 2) = make_float2(-INFINITY, 0.f);
             }
         }
         if (a.cluster) join_cluster();
@@ -767,7 +833,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                 merged[H * DH + H + head] = l;
             }
         } else {
-            const size_t at = (size_t)(b * H + head) * a.p.n_split + split;
+            const size_t at = partial_at(head);
             *reinterpret_cast<float4 *>(a.p.part_o + at * DH + col) = acc;
             if (col == 0) *reinterpret_cast<float2 *>(a.p.part_ml + at * 2) = make_float2(M, l);
         }
@@ -790,12 +856,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     X(8, 16, 1, 128, 2, 2, 1, 1, 4, 1, 2, 8, 1, 2)   \
     X(9, 32, 8, 16, 4, 4, 4, 1, 4, 1, 2, 4, 1, 4)
 
-template <class C>
+template <class C, bool SLOTS>
 cudaError_t launch_cfg(const DecodeArgsP &a, cudaStream_t st) {
-    cudaError_t e = ensure_dynamic_smem<paged_decode_kernel<C>>(C::SMEM);
+    cudaError_t e = ensure_dynamic_smem<paged_decode_kernel<C, SLOTS>>(C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)a.p.n_split, (unsigned)a.p.batch);
+    lc.gridDim = SLOTS ? dim3((unsigned)a.n_slots) : dim3((unsigned)a.p.n_split, (unsigned)a.p.batch);
     lc.blockDim = dim3(C::THREADS);
     lc.dynamicSmemBytes = C::SMEM;
     lc.stream = st;
@@ -808,14 +874,19 @@ cudaError_t launch_cfg(const DecodeArgsP &a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 2;
-    return cudaLaunchKernelEx(&lc, paged_decode_kernel<C>, a);
+    return cudaLaunchKernelEx(&lc, paged_decode_kernel<C, SLOTS>, a);
+}
+
+template <class C>
+cudaError_t launch_split(const DecodeArgsP &a, cudaStream_t st) {
+    return a.p.slots ? launch_cfg<C, true>(a, st) : launch_cfg<C, false>(a, st);
 }
 
 // Clusters of `size` CTAs that can be resident at once on the current device (0: none).
 template <class C>
 int max_clusters(int size) {
-    if (ensure_dynamic_smem<paged_decode_kernel<C>>(C::SMEM) != cudaSuccess) return 0;
-    if (size > 8 && cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+    if (ensure_dynamic_smem<paged_decode_kernel<C, false>>(C::SMEM) != cudaSuccess) return 0;
+    if (size > 8 && cudaFuncSetAttribute(paged_decode_kernel<C, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                         cudaSuccess)
         return 0;
     cudaLaunchConfig_t lc = {};
@@ -830,7 +901,7 @@ int max_clusters(int size) {
     lc.attrs = attr;
     lc.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, paged_decode_kernel<C>, &lc) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, paged_decode_kernel<C, false>, &lc) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -898,19 +969,20 @@ int paged_decode_max_clusters(int variant, bool e4m3, int size) {
 }
 
 cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAttnArgs &p, int groups_per_split,
-                                bool cluster, unsigned long long wait_limit_ns, cudaStream_t st) {
+                                int n_slots, bool cluster, unsigned long long wait_limit_ns, cudaStream_t st) {
     DecodeArgsP a;
     a.p = p;
     a.pool = s.pool;
     a.gps = groups_per_split;
     a.cluster = cluster;
+    a.n_slots = n_slots;
     a.limit_ns = wait_limit_ns;
     cudaError_t e = cudaErrorInvalidValue;
     switch (variant) {
 #define KPA_CASE(IDX, MA, D1, D2, RK, RV, H2, HS, S0, C0, T0, S1, C1, T1)                              \
     case IDX:                                                                                           \
-        e = s.pool.e4m3 ? launch_cfg<Cfg<MA, D1, D2, RK, RV, H2, S1, HS, C1, T1, true>>(a, st)          \
-                        : launch_cfg<Cfg<MA, D1, D2, RK, RV, H2, S0, HS, C0, T0, false>>(a, st);        \
+        e = s.pool.e4m3 ? launch_split<Cfg<MA, D1, D2, RK, RV, H2, S1, HS, C1, T1, true>>(a, st)        \
+                        : launch_split<Cfg<MA, D1, D2, RK, RV, H2, S0, HS, C0, T0, false>>(a, st);      \
         break;
         KPA_PAGED_DECODE_VARIANTS(KPA_CASE)
 #undef KPA_CASE

@@ -489,23 +489,33 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(PagedAttnArgs a, int
     if (rh >= (long long)a.n_rows * h) return;
     const int row = (int)(rh / h);
     if (a.cu && (row < a.cu[0] || row >= a.cu[a.batch])) return;    // a row of no sequence
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + rh * a.n_split;
-    const float *po = a.part_o + rh * a.n_split * dh;
+    long long base = rh * a.n_split, stride = 1;
+    int n = a.n_split;
+    if (a.slots) {
+        const int2 s = a.slots[row];
+        base = (long long)s.x * h + rh % h, stride = h, n = s.y;
+    }
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + base;
+    const float *po = a.part_o + base * dh;
     float M = -INFINITY;
-    for (int z = lane; z < a.n_split; z += 32) M = fmaxf(M, ml[z].x);
+    for (int z = lane; z < n; z += 32) M = fmaxf(M, ml[z * stride].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float l = 0.f;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};                            // features lane + 32 i
+    const int z0 = warp % W;
+    const float2 *mz = ml + z0 * stride;
+    const float *pz = po + z0 * stride * dh + lane;
+    const long long step = W * stride;
 #pragma unroll 4
-    for (int z = warp % W; z < a.n_split; z += W) {
-        const float2 s = ml[z];
+    for (int z = z0; z < n; z += W, mz += step, pz += step * dh) {
+        const float2 s = *mz;
         if (s.x == -INFINITY && s.y == 0.f) continue;
         const float w = exp2f(s.x - M);
         l += w * s.y;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < dh) acc[i] += w * po[(long long)z * dh + lane + 32 * i];
+            if (lane + 32 * i < dh) acc[i] += w * pz[32 * i];
     }
     if constexpr (W > 1) {
 #pragma unroll

@@ -222,7 +222,8 @@ def _prefill(lib, s, fmt, page, past, new, window, sinks, seed, tail=2, max_len=
 
 
 def _decode(lib, s, fmt, page, length, window, sinks, seed, max_len=None):
-    c = pu.Cache(s, fmt, page, length, seed, first_seen=_seen_from([n - 1 for n in length], window), sinks=sinks)
+    c = pu.Cache(s, fmt, page, length, seed, first_seen=_seen_from([n - 1 for n in length], window), sinks=sinks,
+                 stride=None if max_len is None else -(-max_len // page) + 1)
     rng = np.random.default_rng(seed + 1)
     B = len(length)
     q = _q(rng, B, s)
@@ -418,6 +419,33 @@ def test_positions_near_the_end_of_the_range(name):
     _no_error(lib)
     want, tol = pu.attention(c, 0, pu.f64(q[:1]), [n - 1], window, 0, scale, factored=True)
     pu.assert_within(out[:1], want, tol, "decode")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", ["kpa_4x8_8x16_r4", "kpa_4x4_8x8_r2", "tpa_32_64_r1"])
+@pytest.mark.parametrize("length,window", [([3000, 1, 0, 17, 4001, 16], 0), ([9000, 1, 0, 17], 5000), ([0, 0, 0], 0),
+                                           (list(range(0, 400, 2)), 0)], ids=["ragged", "window", "empty", "many"])
+def test_decode_ragged(name, fmt, length, window):
+    """One long sequence among short ones, empty batches, and more sequences than SMs: the
+    blocks size the splits themselves."""
+    _decode(kpa(), SPLITS[name], fmt, 64, length, window, 5 if window else 0, 26, max_len=max(max(length), 30000))
+
+
+def test_bad_lengths_of_a_long_batch():
+    lib = kpa()
+    s = SPLITS["kpa_4x4_8x8_r2"]
+    c = pu.Cache(s, "bf16", 64, [40, 40, 0], 27, stride=400)
+    cfg, pages, scale = lib.make_config(s, "bf16"), c.descriptor(lib), 1.0 / np.sqrt(s.dh)
+    q = _q(np.random.default_rng(28), 3, s)
+    ws = torch.empty(max(256, lib.kpa_paged_decode_workspace_size(cfg, pages, 3, 25600)), dtype=torch.uint8, device="cuda")
+    args = (c.table.cuda(), c.k.cuda(), c.v.cuda(), 25600, 0, 0, scale)
+    for bad in (-1, -2 ** 31):
+        out = torch.full((3, s.h, s.dh), 5.0, dtype=torch.bfloat16, device="cuda")
+        lib.kpa_paged_decode(cfg, pages, 3, q.cuda(), _i32([40, bad, 0]), *args, out, ws)
+        assert lib.kpa_read_device_error() == lib.KPA_ERR_DEVICE_CHECK
+        want, tol = pu.attention(c, 0, pu.f64(q[:1]), [39], 0, 0, scale, factored=True)
+        pu.assert_within(out[:1], want, tol)
+        assert (out[1:] == 0).all()
 
 
 # ------------------------------------------------------------------ together
