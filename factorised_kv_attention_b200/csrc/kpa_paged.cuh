@@ -127,9 +127,10 @@ __device__ __forceinline__ Found find_unit(int idx, const int32_t *cu, const int
 // The same for row tiles of T rows in the order of what they cost: level 0 holds the last
 // tile of every sequence, level 1 the one before it, and so on, sequences in order within a
 // level, so that long rows start first and the last blocks are short.  i is the tile's index
-// from the sequence's front.  (Batches above 256 sequences: sequence after sequence, its last
-// tile first.)
-template <int T>
+// from the sequence's front.  With ShortLast a sequence's last tile comes after all of these where
+// it holds at most T / 2 rows (it costs about half there).  (Batches above 256 sequences:
+// sequence after sequence, its last tile first.)
+template <int T, bool ShortLast = false>
 __device__ __forceinline__ Found find_tile(int idx, const int32_t *cu, const int32_t *start, int batch, int n_rows,
                                            int *err) {
     if (batch > 256) {
@@ -140,6 +141,8 @@ __device__ __forceinline__ Found find_tile(int idx, const int32_t *cu, const int
     __shared__ Found hit;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
+        // a sequence's tiles in the levels: all, or with ShortLast all but a short last one
+        auto levels = [](int n) { return ShortLast ? (n + (T - T / 2 - 1)) / T : (n + T - 1) / T; };
         int n[8], r0[8], pos[8], most = 0, all = 0;                 // sequences lane + 32 k
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -155,44 +158,43 @@ __device__ __forceinline__ Found find_tile(int idx, const int32_t *cu, const int
                     n[k] = r1 - r0[k];
                 }
             }
-            const int t = (n[k] + T - 1) / T;
-            most = max(most, t);
-            all += t;
+            most = max(most, levels(n[k]));
+            all += levels(n[k]);
         }
         most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
         all = (int)__reduce_add_sync(0xffffffffu, (unsigned)all);
         if (lane == 0) hit.b = -1;
         __syncwarp();
-        if (idx < all) {
-            // the largest level whose first unit is no later than idx; before: units of the levels below
-            int lo = 0, hi = most, before = 0;                      // lo is one, hi is not
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                int c = 0;
+        const bool in_levels = idx < all;
+        // the largest level whose first unit is no later than idx; before: units of the levels below
+        int lo = 0, hi = in_levels ? most : 0, before = in_levels ? 0 : all;       // lo is one, hi is not
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            int c = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) c += min((n[k] + T - 1) / T, mid);
-                c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
-                if (c <= idx) {
-                    lo = mid;
-                    before = c;
-                } else {
-                    hi = mid;
-                }
+            for (int k = 0; k < 8; ++k) c += min(levels(n[k]), mid);
+            c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+            if (c <= idx) {
+                lo = mid;
+                before = c;
+            } else {
+                hi = mid;
             }
-            int rank = idx - before;                                // among the sequences that reach the level
+        }
+        int rank = idx - before;                                    // among the sequences that reach the level
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int t = (n[k] + T - 1) / T;
-                const unsigned m = __ballot_sync(0xffffffffu, t > lo);
-                if (t > lo && __popc(m & ((1u << lane) - 1u)) == rank) {
-                    hit.b = lane + 32 * k;
-                    hit.i = t - 1 - lo;
-                    hit.r0 = r0[k];
-                    hit.n = n[k];
-                    hit.pos = pos[k];
-                }
-                rank -= __popc(m);                                  // (negative once found)
+        for (int k = 0; k < 8; ++k) {
+            const int t = levels(n[k]);
+            const bool has = in_levels ? t > lo : (n[k] + T - 1) / T > t;          // (past the levels: a short tile)
+            const unsigned m = __ballot_sync(0xffffffffu, has);
+            if (has && rank >= 0 && __popc(m & ((1u << lane) - 1u)) == rank) {
+                hit.b = lane + 32 * k;
+                hit.i = in_levels ? t - 1 - lo : t;
+                hit.r0 = r0[k];
+                hit.n = n[k];
+                hit.pos = pos[k];
             }
+            rank -= __popc(m);                                      // (negative once found)
         }
     }
     __syncthreads();

@@ -15,9 +15,15 @@
 //   - a tile's 16-slot groups come through the page table: the producer's lanes each load
 //     boxes of as many groups as a page surely holds together (1, 2, 4 or 8), and skip boxes
 //     that no row sees; rebuilt slots that no row sees are zeros;
+//   - a CTA with at most 128 rows has both halves work on them, on tiles in turns, each with
+//     its own maxima, sums and output, joined at the end: a tile then costs its rebuild and not
+//     the chain of a half's products and softmax (9 x 128 rows over 4096 slots, 4 x 4 heads of
+//     8 x 16, R = 2: 90 -> 71 us);
 //   - with d1 = 1 a head's slice of a slot (R (1 + d2) values) is larger than its key, so a
-//     tile is staged and rebuilt in units of 4096 / d_h slots, and as the slice's runs are
-//     long (16 d2 bytes) they come as bulk copies, one per lane;
+//     tile is staged and rebuilt in units of 4096 / d_h slots, by four warps per plane.  The
+//     slice's B rows (contiguous in a group, as h2 = 1) come as one bulk copy per group: a warp
+//     issues its lanes' copies one after the other, and 16 of them took 1600 clocks, longer than
+//     the unit's rebuild (9 x 128 rows, 16 heads of 128, R = 2: 150 -> 100 us);
 //   - an e4m3 token's two scales multiply into its factors before K and V are rounded once to
 //     fp16: in fp32, or at R = 2 in fp16, where factors and products are exact.
 #include <cstring>
@@ -66,23 +72,24 @@ struct Cfg {
     // A unit is what a factor stage holds: US slots in NG layout groups (8 slots, or 16 when e4m3).
     static constexpr int US = TPA ? 4096 / DH : TK, NU = TK / US, NG = US / (E4M3 ? 16 : 8);
     // d1 = 8: blocks of 8 elements x the unit's slots (A_r, then (r, hb) of B), then 32 scale bytes a
-    // group.  d1 = 1: per group R x (A row, D2 B rows) of 16 bytes, then its scale rows.
+    // group.  d1 = 1: per group the B rows of every rank and the scale rows (contiguous in the pool as
+    // h2 = 1: one copy), then (group, r) rows of A.
     static constexpr int BOX = NG * 128, NBLK = R * (1 + HB), FACT = NBLK * BOX;
-    static constexpr int GROUP = R * (1 + D2) * 16 + (E4M3 ? 32 : 0);
-    static constexpr int ST = TPA ? NG * GROUP : FACT + (E4M3 ? NG * 32 : 0);
+    static constexpr int GROUP = R * D2 * 16 + (E4M3 ? 32 : 0), OFF_A = NG * GROUP;
+    static constexpr int ST = TPA ? (OFF_A + NG * R * 16 + 127) / 128 * 128 : FACT + (E4M3 ? NG * 32 : 0);
     // factor stages of a plane: as many as fit beside the Q, K and V tiles (four at most)
     static constexpr size_t OFF_Q = 0;                         // two halves
-    static constexpr size_t OFF_K = OFF_Q + 2 * Q_HALF;        // two buffers
+    static constexpr size_t OFF_K = OFF_Q + 2 * Q_HALF;        // a buffer of K, and the third one
     static constexpr size_t OFF_V = OFF_K + 2 * KV_TILE;       // one buffer
     static constexpr size_t OFF_KST = OFF_V + KV_TILE;
     static constexpr size_t ROOM = 227 * 1024 - 256 - 1024 - 512 - OFF_KST;    // (static memory, alignment, barriers)
     static constexpr int FST = ROOM >= 8 * (size_t)ST && TPA ? 4 : ROOM >= 4 * (size_t)ST ? 2 : 1;
     static constexpr size_t OFF_VST = OFF_KST + (size_t)FST * ST;
     static constexpr size_t OFF_BAR = OFF_VST + (size_t)FST * ST;
-    static constexpr int NBAR = 34;
+    static constexpr int NBAR = 36;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
     static_assert(TPA || D2 == 16 || (D2 == 8 && R == 2), "the fragment mapping covers d2 = 16, and 8 at R = 2");
-    static_assert(!TPA || ((DH == 64 || DH == 128) && NG * R * 2 + (E4M3 ? NG : 0) <= 32), "a unit's copies, one per lane");
+    static_assert(!TPA || ((DH == 64 || DH == 128) && NG * R <= 32), "a unit's copies, one per lane");
     static_assert(ST % 16 == 0 && (TPA || ST % 128 == 0) && OFF_BAR % 8 == 0 && SMEM <= 227 * 1024 - 256, "shared memory");
 };
 
@@ -120,33 +127,49 @@ __device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo
         : "memory");
 }
 
+// The eight softmax warps wait for one another.
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
+}
+
 // mbarrier slots
 enum : int {
     B_Q = 0,
     B_QREADY = 1,      // +h
     B_K_FULL = 3,      // +buffer
     B_K_EMPTY = 5,
-    B_V_FULL = 7,
-    B_V_EMPTY = 8,
-    B_S_FULL = 9,      // +h
-    B_P_HALF = 11,     // +h: the first half of P's columns
-    B_P_FULL = 13,     // +h
-    B_O_FINAL = 15,    // +h
-    B_DRAIN = 17,
-    B_KST_FULL = 18,   // +stage
-    B_VST_FULL = 22,
-    B_KST_EMPTY = 26,
-    B_VST_EMPTY = 30,
+    B_V_FULL = 7,      // +buffer
+    B_V_EMPTY = 9,
+    B_S_FULL = 11,     // +h
+    B_P_HALF = 13,     // +h: the first half of P's columns
+    B_P_FULL = 15,     // +h
+    B_O_FINAL = 17,    // +h
+    B_DRAIN = 19,
+    B_KST_FULL = 20,   // +stage
+    B_VST_FULL = 24,
+    B_KST_EMPTY = 28,
+    B_VST_EMPTY = 32,
 };
 
-// Which local tiles a half works on: both start at 0; half h stops at last[h].
+// What the two halves work on.  With more than 128 rows each half has its own rows and takes
+// every local tile from 0 to its last.  With fewer both have the same rows and take turns on the
+// tiles (alt): step i of half h is tile 2 i + h.
 struct TilePlan {
-    bool act[2];
-    int last[2];
-    int n_kt;
-    __device__ bool active(int h, int t) const { return act[h] && t <= last[h]; }
-    __device__ int first_half(int t) const { return active(0, t) ? 0 : 1; }
-    __device__ int last_half(int t) const { return active(1, t) ? 1 : 0; }
+    bool alt;
+    int steps0, steps1;                           // of each half
+    int n_kt;                                     // tiles of the CTA
+    __device__ int steps(int h) const { return h ? steps1 : steps0; }
+    __device__ bool active(int h, int i) const { return i < steps(h); }
+    __device__ int tile(int h, int i) const { return alt ? 2 * i + h : i; }
+    __device__ bool first_half(int h, int i) const { return alt || h == (active(0, i) ? 0 : 1); }    // on its tile
+    __device__ bool last_half(int h, int i) const { return alt || h == (active(1, i) ? 1 : 0); }
+    // The K and V buffers of a tile and how often each was used before.  There are three, and with alt a
+    // fourth in the place of the query rows 128 .. 255 that there are not.
+    bool k_two, v_two;
+    __device__ int k_buf(int t) const { return k_two ? t & 1 : 0; }
+    __device__ int k_use(int t) const { return k_two ? t >> 1 : t; }
+    __device__ int v_buf(int t) const { return v_two ? t & 1 : 0; }
+    __device__ int v_use(int t) const { return v_two ? t >> 1 : t; }
 };
 
 template <class C>
@@ -170,12 +193,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    const int head = blockIdx.x, split = blockIdx.z;
+    const int head = blockIdx.x, split = blockIdx.y;                // (the parts of the longest tiles start first)
     const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
     const uint64_t limit = a.wait_limit_ns;
 
     // ---- this CTA's rows: rows row0 .. row0 + n - 1 at positions pos0 + r
-    const Found f = find_tile<2 * HQ>(blockIdx.y, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err);
+    const Found f = find_tile<2 * HQ, true>(blockIdx.z, a.p.cu, a.p.start, a.p.batch, a.p.n_rows, a.p.err);
     if (f.b < 0) return;
     const int b = f.b, q0 = f.i * 2 * HQ;
     const int row0 = f.r0 + q0, n = min(2 * HQ, f.n - q0);
@@ -190,53 +213,63 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     int v0, v1;
     split_run(tl.n, split, a.p.n_split, v0, v1);
     TilePlan tp;
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    tp.alt = n <= HQ;
+    // The third buffer is K's second at d1 = 8, where the same warps rebuild K ahead of V.  At d1 = 1, where
+    // V has its own warps and takes them longest, it is V's (d_h = 128, 9 x 256 rows over 4096 slots: 144 us
+    // against 149).
+    tp.k_two = !C::TPA || tp.alt;
+    tp.v_two = C::TPA || tp.alt;
+    auto own_steps = [&](int hh) {                 // tiles that the rows of a half see
         const long long plo = max(pos0 + hh * HQ, 0ll);
         const long long phi = min(pos0 + min(n, (hh + 1) * HQ) - 1, (long long)a.p.max_len - 1);
-        tp.act[hh] = hh * HQ < n && plo <= phi;
-        tp.last[hh] = tp.act[hh] ? min((int)(phi / TK) - tl.gap, v1 - 1) - v0 : -1;
-        if (tp.last[hh] < 0) tp.act[hh] = false, tp.last[hh] = -1;
+        return hh * HQ < n && plo <= phi ? max(min((int)(phi / TK) - tl.gap, v1 - 1) - v0 + 1, 0) : 0;
+    };
+    tp.steps0 = own_steps(0);
+    tp.steps1 = own_steps(1);
+    tp.n_kt = max(tp.steps0, tp.steps1);
+    const bool q0_read = tp.steps0 > 0, q1_read = tp.steps1 > 0;          // which query rows are
+    auto q_read = [&](int hh) { return hh ? q1_read : q0_read; };
+    if (tp.alt) {
+        tp.steps0 = (tp.n_kt + 1) / 2;
+        tp.steps1 = tp.n_kt / 2;
     }
-    tp.n_kt = max(tp.last[0], tp.last[1]) + 1;
+    constexpr uint32_t kThird = (uint32_t)(C::OFF_K + C::KV_TILE), kFourth = (uint32_t)(C::OFF_Q + C::Q_HALF);
+    auto k_off = [&](int t) { return tp.k_buf(t) ? (C::TPA ? kFourth : kThird) : (uint32_t)C::OFF_K; };
+    auto v_off = [&](int t) { return tp.v_buf(t) ? (C::TPA ? kThird : kFourth) : (uint32_t)C::OFF_V; };
     auto seen = [&](int s) { return s <= hi && (s >= wstart || s < a.p.mask.sinks); };
 
     // ---- producers' side (one warp per plane): page lookups and copies
     const bool is_producer = warp >= kProducerWarp, prod_v = warp == kProducerWarp + 1;
     const int bg = a.box_groups, nb = TK / 16 / bg;               // boxes of a tile
     const int rows = E4M3 ? bg : 2 * bg;                          // layout groups of a box
-    // The page of this lane's copies of unit u (d1 = 8: box `lane` of the tile; d1 = 1: its own copy's
-    // group), not looked at yet, and the first 16-slot group inside it (-1: nothing, or seen by no row)
-    constexpr int CPG = C::R * 2;                                 // d1 = 1: copies of a group, A and B per rank
-    const int my_group = !C::TPA ? lane : lane < C::NG * CPG ? lane / CPG : E4M3 ? lane - C::NG * CPG : C::NG;
+    // Pages are looked up for 32 runs of slots at a time (a load waited for at every unit would cost the
+    // warp more than its copies): lane l holds run l % n_runs of unit u + l / n_runs.  A run is a box at
+    // d1 = 8, a group of the unit at d1 = 1.  in_page: its first 16-slot group inside its page (-1: nothing,
+    // or seen by no row).
+    const int n_runs = C::TPA ? C::NG : nb, units = 32 / n_runs;          // (powers of two)
     int page = 0, in_page = -1;
-    auto fetch = [&](int u) {
+    auto fetch = [&](int u0) {
         in_page = -1;
-        const int t = u / C::NU;
-        if (my_group >= (C::TPA ? C::NG : nb) || t >= tp.n_kt) return;
+        const int u = u0 + lane / n_runs, t = u / C::NU;
+        if (t >= tp.n_kt) return;
         const int span = C::TPA ? (E4M3 ? 16 : 8) : bg * 16;
-        const int s0 = tl.slot_tile(v0 + t) * TK + (u % C::NU) * C::US + my_group * span;
+        const int s0 = tl.slot_tile(v0 + t) * TK + (u % C::NU) * C::US + lane % n_runs * span;
         if (s0 > hi || (s0 + span <= wstart && s0 >= a.p.mask.sinks)) return;
         int entry;
         split_group(a.pool, s0 >> 4, entry, in_page);
         page = __ldg(a.pool.table + (size_t)b * a.pool.table_stride + entry);
     };
     // copies of this lane: box (lane + 32 j) % nb of block (lane + 32 j) / nb
-    // (d1 = 1: the lane's one copy: its offset in a 16-slot group of the pool, in the unit, and size)
+    // (d1 = 1: the lane's group's B rows, and one A row of group lane / R: byte offsets in a 16-slot group)
     constexpr int CP = C::TPA ? 1 : (C::NBLK * 8 + 31) / 32;
     int cp_x[CP], cp_dst[CP], cp_box[CP];
     auto plan_copies = [&] {
         const int ab = R * a.h1 * D1;                             // first B element of a record
         if constexpr (C::TPA) {
-            const int gb = prod_v ? a.pool.vg : a.pool.kg;
-            const int c = lane % CPG, r = c >> 1;
-            if (lane >= C::NG * CPG) {                            // the scale rows
-                cp_x[0] = gb - 32, cp_dst[0] = my_group * C::GROUP + C::GROUP - 32, cp_box[0] = 32;
-            } else {
-                cp_x[0] = ((c & 1) ? ab + (r * a.h2 + i2) * C::D2 : r * a.h1 + i1) * 16 + (!E4M3 && (my_group & 1) ? gb / 2 : 0);
-                cp_dst[0] = my_group * C::GROUP + (r * (1 + C::D2) + (c & 1)) * 16;
-                cp_box[0] = (c & 1) ? C::D2 * 16 : 16;
-            }
+            const int half = (prod_v ? a.pool.vg : a.pool.kg) / 2;        // of the two 8-slot groups of a bf16 one
+            cp_x[0] = ab * 16 + (!E4M3 && (lane & 1) ? half : 0);
+            cp_dst[0] = lane * C::GROUP;
+            cp_box[0] = ((lane % R) * a.h1 + i1) * 16 + (!E4M3 && (lane / R & 1) ? half : 0);
             return;
         }
 #pragma unroll
@@ -249,27 +282,31 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             cp_dst[j] = k * C::BOX + cp_box[j] * rows * 128;
         }
     };
-    // the head's factor slices of unit u (its pages fetched) into its stage, which is free
+    // the head's factor slices of unit u (its pages looked up) into its stage, which is free
     auto copy_factors = [&](int u) {
-        long long grp = -1;
-        if (in_page >= 0) {
-            if (page < 0 || page >= a.pool.n_pages) {
-                raise_error(a.p.err, kErrDeviceCheck);
-                page = 0;
-            }
-            grp = (long long)page * a.pool.pg + in_page;
+        const int from = (u & (units - 1)) * n_runs + (lane & (n_runs - 1));
+        const int pu = __shfl_sync(0xffffffffu, page, from), iu = __shfl_sync(0xffffffffu, in_page, from);
+        long long grp = -1;                                       // (lane < n_runs) first group of this lane's run
+        if (lane < n_runs && iu >= 0) {
+            const bool bad = pu < 0 || pu >= a.pool.n_pages;
+            if (bad) raise_error(a.p.err, kErrDeviceCheck);
+            grp = (long long)(bad ? 0 : pu) * a.pool.pg + iu;
         }
         const int s = u % C::FST;
         const uint32_t full = bar((prod_v ? B_VST_FULL : B_KST_FULL) + s);
         const uint32_t st = smem_u32(smem + (prod_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
         if constexpr (C::TPA) {
-            const unsigned bytes = __reduce_add_sync(0xffffffffu, grp >= 0 ? (unsigned)cp_box[0] : 0u);
-            if (lane == 0) mbar_expect_tx(full, bytes);
+            // The B rows as one bulk copy per group (each costs its warp about 100 clocks, one lane after the
+            // other), the 16-byte A rows as plain asynchronous copies; every lane arrives for its own.
+            const unsigned char *plane = prod_v ? a.pool.v : a.pool.k;
+            const size_t gbytes = prod_v ? a.pool.vg : a.pool.kg;
+            const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
+            if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * C::GROUP);
             __syncwarp();
-            if (grp >= 0)
-                sm100::bulk_g2s(st + cp_dst[0],
-                                (prod_v ? a.pool.v + (size_t)grp * a.pool.vg : a.pool.k + (size_t)grp * a.pool.kg) + cp_x[0],
-                                (uint32_t)cp_box[0], full);
+            if (grp >= 0) sm100::bulk_g2s(st + cp_dst[0], plane + (size_t)grp * gbytes + cp_x[0], C::GROUP, full);
+            const long long ga = __shfl_sync(0xffffffffu, grp, lane / R % C::NG);
+            if (lane < C::NG * R && ga >= 0) sm100::cp_async16(st + C::OFF_A + lane * 16, plane + (size_t)ga * gbytes + cp_box[0]);
+            sm100::cp_async_arrive(full);
             return;
         }
         const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
@@ -301,16 +338,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             for (int i = 0; i < C::NBAR; ++i) {
                 uint32_t count = 1;
                 if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_HALF && i < B_P_FULL + 2)) count = 4;
-                if (i >= B_KST_EMPTY || (i >= B_K_FULL && i < B_K_FULL + 2) || i == B_V_FULL) count = kRebuildWarps;
+                if (C::TPA && i >= B_KST_FULL && i < B_KST_EMPTY) count = 1 + 32;
+                if (i >= B_KST_EMPTY || (i >= B_K_FULL && i < B_K_FULL + 2) || (i >= B_V_FULL && i < B_V_FULL + 2)) count = C::TPA ? kRebuildWarps / 2 : kRebuildWarps;
                 mbar_init(bar(i), count);
             }
             *abort_flag = 0;
             mbar_fence_init();
             if (tp.n_kt > 0) {
-                mbar_expect_tx(bar(B_Q), (uint32_t)((tp.act[0] ? 1 : 0) + (tp.act[1] ? 1 : 0)) * C::Q_HALF);
+                mbar_expect_tx(bar(B_Q), (uint32_t)((q0_read ? 1 : 0) + (q1_read ? 1 : 0)) * C::Q_HALF);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
-                    if (tp.act[hh])
+                    if (q_read(hh))
 #pragma unroll
                         for (int cb = 0; cb < DH / 64; ++cb)
                             tma_load_2d(smem_u32(smem + C::OFF_Q + hh * C::Q_HALF + cb * HQ * 128), &tmq,
@@ -344,19 +382,35 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         }
     };
 
+    // The same by a whole warp: its lanes stay together, and the first polls do without the timer.
+    auto wait_warp = [&](int i, uint32_t parity) -> bool {
+        uint64_t t0 = 0;
+        for (uint32_t it = 1;; ++it) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
+            if ((it & 15) == 0) {
+                const uint64_t now = globaltimer();
+                if (it == 16) t0 = now;
+                const bool late = now - t0 > limit;
+                if (late && lane == 0 && !*abort_flag) {
+                    *abort_flag = 1;
+                    raise_error(a.p.err, kErrTimeout);
+                }
+                if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+            }
+        }
+    };
+
     if (is_producer) {
         // ---------------------------------------------------------------- producers
         if (tp.n_kt > 0) {
             const int b_empty = prod_v ? B_VST_EMPTY : B_KST_EMPTY, b_full = prod_v ? B_VST_FULL : B_KST_FULL;
             if (prod_v) copy_factors(0);
-            fetch(1);                                             // (waited for at its use)
             int issued = 0;
             for (int u = 1; u < tp.n_kt * C::NU; ++u) {
-                const bool ok = u < C::FST || wait(b_empty + u % C::FST, ((u / C::FST) - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if ((u & (units - 1)) == 0) fetch(u);
+                if (u >= C::FST && !wait_warp(b_empty + u % C::FST, ((u / C::FST) - 1) & 1)) break;
                 copy_factors(u);
                 issued = u;
-                fetch(u + 1);
             }
             // every copy this warp started lands before the CTA can exit
             if (!prod_v) (void)mbar_wait(bar(B_Q), 0, limit);
@@ -370,46 +424,50 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             bool ok = true;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
-                if (ok && tp.act[hh] && !wait(B_QREADY + hh, 0)) ok = false;
-            const uint32_t d_q = umma_lo(smem_u32(smem + C::OFF_Q)), d_k = umma_lo(smem_u32(smem + C::OFF_K)),
-                           d_v = umma_lo(smem_u32(smem + C::OFF_V));
-            auto issue_s = [&](int hh, int t) -> bool {
-                const int kb = t & 1;
-                if (!wait(B_K_FULL + kb, (t >> 1) & 1)) return false;
+                if (ok && q_read(hh) && !wait(B_QREADY + hh, 0)) ok = false;
+            const uint32_t d_q = umma_lo(smem_u32(smem + C::OFF_Q)), d_0 = umma_lo(smem_u32(smem));
+            // step i of half hh
+            auto issue_s = [&](int hh, int i) -> bool {
+                const int t = tp.tile(hh, i), kb = tp.k_buf(t);
+                if (!wait(B_K_FULL + kb, tp.k_use(t) & 1)) return false;
                 tc_fence_after();
-            const uint32_t q_lo = d_q + hh * (C::Q_HALF >> 4), k_lo = d_k + kb * (C::KV_TILE >> 4), s_addr = tmem + hh * 128;
+                const uint32_t q_lo = tp.alt ? d_q : d_q + hh * (C::Q_HALF >> 4), k_lo = d_0 + (k_off(t) >> 4);
+                const uint32_t s_addr = tmem + hh * 128;
 #pragma unroll
-            for (int k = 0; k < DH / 16; ++k)
-                umma_ss(s_addr, q_lo + (k / 4) * (HQ * 128 >> 4) + 2 * (k % 4), k_lo + (k / 4) * (TK * 128 >> 4) + 2 * (k % 4),
-                        idesc_s, k > 0);
+                for (int k = 0; k < DH / 16; ++k)
+                    umma_ss(s_addr, q_lo + (k / 4) * (HQ * 128 >> 4) + 2 * (k % 4), k_lo + (k / 4) * (TK * 128 >> 4) + 2 * (k % 4),
+                            idesc_s, k > 0);
                 umma_commit(bar(B_S_FULL + hh));
-                if (hh == tp.last_half(t)) umma_commit(bar(B_K_EMPTY + kb));
+                if (tp.last_half(hh, i)) umma_commit(bar(B_K_EMPTY + kb));
                 return true;
             };
-            auto issue_pv = [&](int hh, int t) -> bool {
-                if (!wait(B_P_HALF + hh, t & 1)) return false;
-                if (hh == tp.first_half(t) && !wait(B_V_FULL, t & 1)) return false;
+            auto issue_pv = [&](int hh, int i) -> bool {
+                const int t = tp.tile(hh, i), vb = tp.v_buf(t);
+                if (!wait(B_P_HALF + hh, i & 1)) return false;
+                if (tp.first_half(hh, i) && !wait(B_V_FULL + vb, tp.v_use(t) & 1)) return false;
                 tc_fence_after();
+                const uint32_t v_lo = d_0 + (v_off(t) >> 4);
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k) {
                     if (k == TK / 32) {                               // the rest of P
-                        if (!wait(B_P_FULL + hh, t & 1)) return false;
+                        if (!wait(B_P_FULL + hh, i & 1)) return false;
                         tc_fence_after();
                     }
-                    umma_ts_lo(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, d_v + (k / 4) * (DH * 128 >> 4) + 2 * (k % 4), idesc_o, t > 0 || k > 0);
+                    umma_ts_lo(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, v_lo + (k / 4) * (DH * 128 >> 4) + 2 * (k % 4), idesc_o,
+                               i > 0 || k > 0);
                 }
-                if (hh == tp.last_half(t)) umma_commit(bar(B_V_EMPTY));
-                if (t == tp.last[hh]) umma_commit(bar(B_O_FINAL + hh));
+                if (tp.last_half(hh, i)) umma_commit(bar(B_V_EMPTY + vb));
+                if (i == tp.steps(hh) - 1) umma_commit(bar(B_O_FINAL + hh));
                 return true;
             };
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
                 if (ok && tp.active(hh, 0)) ok = issue_s(hh, 0);
-            for (int t = 0; t < tp.n_kt && ok; ++t) {
+            for (int i = 0; i < max(tp.steps0, tp.steps1) && ok; ++i) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    if (ok && tp.active(hh, t)) ok = issue_pv(hh, t);
-                    if (ok && tp.active(hh, t + 1)) ok = issue_s(hh, t + 1);
+                    if (ok && tp.active(hh, i)) ok = issue_pv(hh, i);
+                    if (ok && tp.active(hh, i + 1)) ok = issue_s(hh, i + 1);
                 }
             }
             // nothing issued here may still run when tensor memory is released
@@ -426,7 +484,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             constexpr bool is_v = decltype(v_c)::value;
             const int fs = (t * C::NU + j) % C::FST;
             const unsigned char *st = smem + (is_v ? C::OFF_VST : C::OFF_KST) + (size_t)fs * C::ST;
-            const uint32_t dst = smem_u32(smem + (is_v ? C::OFF_V : C::OFF_K + (t & 1) * C::KV_TILE));
+            const uint32_t dst = smem_u32(smem) + (is_v ? v_off(t) : k_off(t));
             const int t0 = tl.slot_tile(v0 + t) * TK;
             const bool edge = !(t0 + TK - 1 <= hi && t0 >= wstart);
             // the exact fp16 scales of an e4m3 group's slots tok and tok + 8 (scale rows at e): half of each
@@ -450,65 +508,72 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     stsm_x4_t(dst + (g >> 3) * (DH * 128) + sw128_chunk(f0 + brow, g & 7), w[0], w[1], w[2], w[3]);
             };
             if constexpr (C::TPA && !E4M3) {
-                // one 8-slot group and 64 features per warp
-                constexpr int FP = 8 / C::NG;                      // warps per group
-                const int gu = rw / FP, fp = rw % FP, g = j * C::NG + gu;
-                const unsigned char *grp = st + gu * C::GROUP;
-                float av[R];
+                // two pieces of one 8-slot group and 64 features per warp
+                constexpr int FP = 8 / C::NG;                      // pieces of a group
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    av[r] = __uint_as_float(
-                        (uint32_t)(*reinterpret_cast<const uint16_t *>(grp + r * (1 + C::D2) * 16 + 2 * tok)) << 16);
-                const bool zero = edge && !seen(t0 + g * kGroup + tok);
+                for (int pc = 0; pc < 2; ++pc) {
+                    const int at = 2 * (rw & 3) + pc, gu = at / FP, fp = at % FP, g = j * C::NG + gu;
+                    const unsigned char *ga = st + C::OFF_A + gu * R * 16, *gb = st + gu * C::GROUP;
+                    float av[R];
 #pragma unroll
-                for (int q4 = 0; q4 < 2; ++q4) {
-                    const int f0 = fp * 64 + (q4 * 4 + blk) * 8;
-                    float2 acc[4];
+                    for (int r = 0; r < R; ++r)
+                        av[r] = __uint_as_float(
+                            (uint32_t)(*reinterpret_cast<const uint16_t *>(ga + r * 16 + 2 * tok)) << 16);
+                    const bool zero = edge && !seen(t0 + g * kGroup + tok);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        uint32_t bw[4];
-                        ldsm_x4_t(smem_u32(grp + (r * (1 + C::D2) + 1 + f0 + brow) * 16), bw);
+                    for (int q4 = 0; q4 < 2; ++q4) {
+                        const int f0 = fp * 64 + (q4 * 4 + blk) * 8;
+                        float2 acc[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 a2 = make_float2(av[r], av[r]), x = unpack_bf16x2(bw[i]);
-                            acc[i] = r == 0 ? fmul2(a2, x) : ffma2(a2, x, acc[i]);
+                        for (int r = 0; r < R; ++r) {
+                            uint32_t bw[4];
+                            ldsm_x4_t(smem_u32(gb + (r * C::D2 + f0 + brow) * 16), bw);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 a2 = make_float2(av[r], av[r]), x = unpack_bf16x2(bw[i]);
+                                acc[i] = r == 0 ? fmul2(a2, x) : ffma2(a2, x, acc[i]);
+                            }
                         }
-                    }
-                    uint32_t w[4];
+                        uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = zero ? 0u : pack_half2(acc[i].x, acc[i].y);
-                    store_blocks(g, f0, w);
+                        for (int i = 0; i < 4; ++i) w[i] = zero ? 0u : pack_half2(acc[i].x, acc[i].y);
+                        store_blocks(g, f0, w);
+                    }
                 }
                 return;
             }
             if constexpr (C::TPA && E4M3) {
-                // one 16-slot group and 32 features per warp, slots tok and tok + 8 per lane (see below)
+                // two pieces of one 16-slot group and 32 features per warp, slots tok and tok + 8 per lane (see below)
                 constexpr int FP = 8 / C::NG;
-                const int gu = rw / FP, fp = rw % FP, g = 2 * (j * C::NG + gu), f0 = fp * 32 + blk * 8;
-                const unsigned char *grp = st + gu * C::GROUP;
-                uint32_t sa2, sb_lo, sb_hi, w[2][4];
-                paired_scales(grp + C::GROUP - 32 + 2 * tok, sa2, sb_lo, sb_hi);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const uint32_t x =
-                        hmul2(e4m3x2_to_h2(*reinterpret_cast<const uint16_t *>(grp + r * (1 + C::D2) * 16 + 2 * tok)), sa2);
-                    const uint32_t a_lo = __byte_perm(x, 0, 0x1010), a_hi = __byte_perm(x, 0, 0x3232);
-                    uint32_t bw[4];
-                    ldsm_x4_t(smem_u32(grp + (r * (1 + C::D2) + 1 + f0 + brow) * 16), bw);
+                for (int pc = 0; pc < 2; ++pc) {
+                    const int at = 2 * (rw & 3) + pc, gu = at / FP, fp = at % FP;
+                    const int g = 2 * (j * C::NG + gu), f0 = fp * 32 + blk * 8;
+                    const unsigned char *ga = st + C::OFF_A + gu * R * 16, *gb = st + gu * C::GROUP;
+                    uint32_t sa2, sb_lo, sb_hi, w[2][4];
+                    paired_scales(gb + C::GROUP - 32 + 2 * tok, sa2, sb_lo, sb_hi);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t lo2, hi2;
-                        e4m3_split(bw[i], lo2, hi2);
-                        lo2 = hmul2(lo2, sb_lo);
-                        hi2 = hmul2(hi2, sb_hi);
-                        w[0][i] = r == 0 ? hmul2(a_lo, lo2) : hfma2(a_lo, lo2, w[0][i]);
-                        w[1][i] = r == 0 ? hmul2(a_hi, hi2) : hfma2(a_hi, hi2, w[1][i]);
+                    for (int r = 0; r < R; ++r) {
+                        const uint32_t x =
+                            hmul2(e4m3x2_to_h2(*reinterpret_cast<const uint16_t *>(ga + r * 16 + 2 * tok)), sa2);
+                        const uint32_t a_lo = __byte_perm(x, 0, 0x1010), a_hi = __byte_perm(x, 0, 0x3232);
+                        uint32_t bw[4];
+                        ldsm_x4_t(smem_u32(gb + (r * C::D2 + f0 + brow) * 16), bw);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t lo2, hi2;
+                            e4m3_split(bw[i], lo2, hi2);
+                            lo2 = hmul2(lo2, sb_lo);
+                            hi2 = hmul2(hi2, sb_hi);
+                            w[0][i] = r == 0 ? hmul2(a_lo, lo2) : hfma2(a_lo, lo2, w[0][i]);
+                            w[1][i] = r == 0 ? hmul2(a_hi, hi2) : hfma2(a_hi, hi2, w[1][i]);
+                        }
                     }
-                }
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (edge && !seen(t0 + (g + hf) * kGroup + tok)) w[hf][0] = w[hf][1] = w[hf][2] = w[hf][3] = 0u;
-                    store_blocks(g + hf, f0, w[hf]);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (edge && !seen(t0 + (g + hf) * kGroup + tok)) w[hf][0] = w[hf][1] = w[hf][2] = w[hf][3] = 0u;
+                        store_blocks(g + hf, f0, w[hf]);
+                    }
                 }
                 return;
             }
@@ -642,18 +707,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         // replaces done
         auto unit = [&](int t, int j, auto v_c) -> bool {
             constexpr bool is_v = decltype(v_c)::value;
-            const int s = t & 1, u = t * C::NU + j, fs = u % C::FST;      // K buffer, factor stage
+            const int u = t * C::NU + j, fs = u % C::FST;                 // factor stage
             bool ok = true;
-            if (j == 0 && !is_v && t >= 2) ok = wait(B_K_EMPTY + s, ((t >> 1) - 1) & 1);
-            if (j == 0 && is_v && t >= 1) ok = wait(B_V_EMPTY, (t - 1) & 1);
-            if (ok) ok = wait((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1);
-            if (!__all_sync(0xffffffffu, ok)) return false;
+            if (j == 0 && !is_v && tp.k_use(t) >= 1) ok = wait_warp(B_K_EMPTY + tp.k_buf(t), (tp.k_use(t) - 1) & 1);
+            if (j == 0 && is_v && tp.v_use(t) >= 1) ok = wait_warp(B_V_EMPTY + tp.v_buf(t), (tp.v_use(t) - 1) & 1);
+            if (!ok || !wait_warp((is_v ? B_VST_FULL : B_KST_FULL) + fs, (u / C::FST) & 1)) return false;
             rebuild(t, j, v_c);
             if (j == C::NU - 1) fence_async_smem();         // visible to the tensor cores
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar((is_v ? B_VST_EMPTY : B_KST_EMPTY) + fs));
-                if (j == C::NU - 1) mbar_arrive(bar(is_v ? B_V_FULL : B_K_FULL + s));
+                if (j == C::NU - 1) mbar_arrive(bar(is_v ? B_V_FULL + tp.v_buf(t) : B_K_FULL + tp.k_buf(t)));
             }
             return true;
         };
@@ -668,21 +732,35 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             }
             return ok;
         };
-        bool ok = tp.n_kt > 0;
-        for (int t = -1; t < tp.n_kt && ok; ++t) ok = both(t + 1, t);
+        if constexpr (C::TPA) {
+            // d1 = 1: four warps per plane (a unit is little work for eight)
+            auto plane = [&](auto v_c) {
+                bool ok = true;
+#pragma unroll 1
+                for (int u = 0; u < tp.n_kt * C::NU && ok; ++u) ok = unit(u / C::NU, u % C::NU, v_c);
+            };
+            if (rw < kRebuildWarps / 2)
+                plane(std::false_type{});
+            else
+                plane(std::true_type{});
+        } else {
+            bool ok = tp.n_kt > 0;
+            for (int t = -1; t < tp.n_kt && ok; ++t) ok = both(t + 1, t);
+        }
     } else {
         // ---------------------------------------------------------------- softmax rows
         const int hh = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane, r = hh * HQ + row;
+        const int hq = tp.alt ? 0 : hh * HQ;                             // the half's first row
+        const int row = quarter * 32 + lane, r = hq + row;
         const bool exists = r < n;
         const long long at = pos0 + r;
         const bool live = exists && at >= 0 && at < a.p.max_len;
         const size_t rh = (size_t)(row0 + r) * h + head;
-        if (tp.act[hh]) {
+        if (tp.steps(hh) > 0) {
             // Q_h: bf16 -> fp16 x qscale in place, once its copy has landed
-            bool ok = wait(B_Q, 0);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
+            bool ok = true;
+            if (q_read(hh)) ok = wait_warp(B_Q, 0);
+            if (ok && q_read(hh)) {
                 uint4 *q4 = reinterpret_cast<uint4 *>(smem + C::OFF_Q + hh * C::Q_HALF);
 #pragma unroll 4
                 for (int i = row; i < (int)(C::Q_HALF / 16); i += HQ) {
@@ -705,15 +783,15 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             const uint32_t o_addr = tmem + lane_off + 256 + hh * 128;
             const int pos = live ? (int)at : -1;                         // (-1 sees nothing)
             const int wlow = window_start(a.p.mask, pos);
-            const int half_lo = (int)max(pos0 + hh * HQ, 0ll);           // smallest position of the half
-            const int half_w = window_start(a.p.mask, (int)min(pos0 + min(n, (hh + 1) * HQ) - 1, (long long)hi));
-            const bool all_live = pos0 + hh * HQ >= 0 && pos0 + min(n, (hh + 1) * HQ) <= a.p.max_len;
+            const int half_lo = (int)max(pos0 + hq, 0ll);                // smallest position of the half
+            const int half_w = window_start(a.p.mask, (int)min(pos0 + min(n, hq + HQ) - 1, (long long)hi));
+            const bool all_live = pos0 + hq >= 0 && pos0 + min(n, hq + HQ) <= a.p.max_len;
             float m_used = -INFINITY, l_run = 0.f;
-            for (int t = 0; t <= tp.last[hh] && ok; ++t) {
-                ok = __all_sync(0xffffffffu, wait(B_S_FULL + hh, t & 1));
+            for (int i = 0; i < tp.steps(hh) && ok; ++i) {
+                ok = wait_warp(B_S_FULL + hh, i & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const int t0 = tl.slot_tile(v0 + t) * TK;
+                const int t0 = tl.slot_tile(v0 + tp.tile(hh, i)) * TK;
                 const bool masked = t0 + TK - 1 > half_lo || t0 < half_w || !all_live;
                 // slots j <= lim of the tile, from low on or below sink, are visible
                 const int lim = pos - t0, low = wlow - t0, sink = a.p.mask.sinks - t0;
@@ -748,7 +826,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     m_used = mx;
                     l_run *= alpha;
                 }
-                if (t > 0 && __any_sync(0xffffffffu, grow)) {
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
                     for (int c = 0; c < DH / 32; ++c) {
                         float v[32];
@@ -796,28 +874,57 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_P_FULL + hh));
             }
-            // epilogue: one row per thread, normalised or as this split's partial
-            if (ok) ok = __all_sync(0xffffffffu, wait(B_O_FINAL + hh, 0));
+            // epilogue: one row per thread, normalised or as this split's partial.  Halves that took turns
+            // first join their maxima and sums (in a factor stage, whose last unit is long rebuilt); then each
+            // writes half of the columns of both.
+            const bool join = tp.alt && tp.steps1 > 0;
+            if (ok) ok = wait_warp(B_O_FINAL + hh, 0);
+            float m_row = m_used, l_row = l_run, w_own = 1.f, w_other = 0.f;
+            if (join) {
+                float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_KST);
+                if (ok) ok = wait_warp(B_O_FINAL + (hh ^ 1), 0);
+                if (ok) ml[hh * HQ + row] = make_float2(m_used, l_run);
+                softmax_sync();
+                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+                const float2 o = ml[(hh ^ 1) * HQ + row];
+                m_row = fmaxf(m_used, o.x);
+                w_own = m_used == -INFINITY ? 0.f : ex2(m_used - m_row);
+                w_other = o.x == -INFINITY ? 0.f : ex2(o.x - m_row);
+                l_row = l_run * w_own + o.y * w_other;
+            }
+            const bool whole = a.p.n_split == 1;
+            // Rows go out through the query tile, which no product reads any more: a thread's row is
+            // strided by h d_h in memory, a row's 16-byte pieces by lanes are whole lines.
+            constexpr int kRow = DH * 2;                                 // bytes of a bf16 row
+            unsigned char *stage = smem + C::OFF_Q + hq * kRow + quarter * 32 * kRow;
             if (ok) {
                 tc_fence_after();
                 bool finite = true;
-                const bool whole = a.p.n_split == 1;
-                const float inv = !whole ? 1.f : (l_run == 0.f ? 0.f : a.p.out_scale / l_run);
-                if (!whole && exists) {
+                const float inv = !whole ? 1.f : (l_row == 0.f ? 0.f : a.p.out_scale / l_row);
+                if (!whole && exists && !(join && hh)) {
                     *reinterpret_cast<float2 *>(a.p.part_ml + (rh * a.p.n_split + split) * 2) =
-                        make_float2(live ? m_used : -INFINITY, live ? l_run : 0.f);
-                    finite = !live || (l_run <= 3.4e38f && m_used <= 3.4e38f);
+                        make_float2(live ? m_row : -INFINITY, live ? l_row : 0.f);
+                    finite = !live || (l_row <= 3.4e38f && m_row <= 3.4e38f);
                 }
-                // Rows go out through the half's own query tile, which no product reads any more: a
-                // thread's row is strided by h d_h in memory, a row's 16-byte pieces by lanes are whole lines.
-                constexpr int kRow = DH * 2;                             // bytes of a bf16 row
-                unsigned char *stage = smem + C::OFF_Q + hh * C::Q_HALF + quarter * 32 * kRow;
+                w_own *= inv, w_other *= inv;
+                const int c0 = join ? hh * (DH / 64) : 0, c1 = join ? c0 + DH / 64 : DH / 32;
 #pragma unroll 1
-                for (int c = 0; c < DH / 32; ++c) {
+                for (int c = c0; c < c1; ++c) {
                     float v[32];
                     tmem_ld32(o_addr + c * 32, v);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * inv : 0.f;
+                    for (int j = 0; j < 32; ++j) v[j] *= w_own;
+                    if (join) {
+#pragma unroll
+                        for (int j0 = 0; j0 < 32; j0 += 16) {
+                            float o[16];
+                            sm100::tmem_ld16(tmem + lane_off + 256 + (hh ^ 1) * 128 + c * 32 + j0, o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j0 + j] += o[j] * w_other;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = live ? v[j] : 0.f;
                     if (exists) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) finite &= fabsf(v[j]) <= 3.4e38f;
@@ -839,19 +946,23 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                                 make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                     }
                 }
-                if (whole) {
-                    __syncwarp();
-                    constexpr int LPR = kRow / 16;                       // lanes per row
-                    const int piece = lane % LPR, first = quarter * 32 + hh * HQ;
-#pragma unroll 4
-                    for (int i = lane / LPR; i < 32; i += 32 / LPR)
-                        if (first + i < n)
-                            *reinterpret_cast<uint4 *>(a.p.out + ((size_t)(row0 + first + i) * h + head) * DH + piece * 8) =
-                                *reinterpret_cast<const uint4 *>(stage + i * kRow + ((piece ^ (i & 7)) << 4));
-                }
                 if (!finite) raise_error(a.p.err, kErrDeviceCheck);
             }
-        } else if (exists) {                                          // no tile of this half here
+            if (whole) {
+                if (join)
+                    softmax_sync();                                      // the other half's columns
+                else
+                    __syncwarp();
+                constexpr int LPR = kRow / 16;                           // lanes per row
+                const int piece = lane % LPR, first = quarter * 32 + hq;
+                const int i0 = join ? hh * 16 : 0, i1 = join ? i0 + 16 : 32;     // this warp's rows of the quarter
+#pragma unroll 4
+                for (int i = i0 + lane / LPR; i < i1; i += 32 / LPR)
+                    if (ok && first + i < n)
+                        *reinterpret_cast<uint4 *>(a.p.out + ((size_t)(row0 + first + i) * h + head) * DH + piece * 8) =
+                            *reinterpret_cast<const uint4 *>(stage + i * kRow + ((piece ^ (i & 7)) << 4));
+            }
+        } else if (exists && !(tp.alt && hh)) {                       // no tile of this half's rows here
             if (a.p.n_split > 1) {
                 *reinterpret_cast<float2 *>(a.p.part_ml + (rh * a.p.n_split + split) * 2) = make_float2(-INFINITY, 0.f);
             } else {
@@ -903,7 +1014,7 @@ cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned lon
     cudaError_t e = ensure_dynamic_smem<paged_prefill_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)(((long long)p.n_rows + (long long)p.batch * (2 * HQ - 1)) / (2 * HQ));
-    paged_prefill_kernel<C><<<dim3((unsigned)s.d.h, tiles, (unsigned)p.n_split), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
+    paged_prefill_kernel<C><<<dim3((unsigned)s.d.h, (unsigned)p.n_split, tiles), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.n_split == 1) return e;
     return launch_paged_combine(s, p, st);
@@ -917,7 +1028,7 @@ bool paged_prefill_supported(const PagedShape &s) {
     const Dims &d = s.d;
     // group coordinates of the tensor maps are 32-bit
     if ((uint64_t)s.pool.n_pages * s.pool.pg * 2 > INT32_MAX || d.rk != d.rv) return false;
-    if (d.d1 == 1) return (d.d2 == 64 && d.rk <= 2) || (d.d2 == 128 && d.rk == 2);
+    if (d.d1 == 1) return d.h2 == 1 && ((d.d2 == 64 && d.rk <= 2) || (d.d2 == 128 && d.rk == 2));
     return d.d1 == 8 && ((d.d2 == 16 && (d.rk == 2 || d.rk == 4)) || (d.d2 == 8 && d.rk == 2));
 }
 

@@ -267,6 +267,18 @@ def test_prefill_long_past(page, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("new,past,window,sinks", [
+    ([1, 127, 128, 129], [0, 1, 0, 0], 0, 0),                 # one or two key tiles
+    ([1, 1, 1, 1, 1], [127, 128, 255, 256, 383], 0, 0),       # an odd and an even number of them
+    ([3, 128, 64, 256 + 1, 256 + 128, 256 + 129], [700, 333, 512, 450, 100, 0], 0, 0),
+    ([1, 2, 300], [5000, 4000, 2500], 0, 0),                  # split over the keys
+    ([1, 100, 128, 270], [3000, 2000, 1030, 900], 200, 130)], ids=["one", "tiles", "short", "split", "window"])
+def test_prefill_few_rows(name, fmt, new, past, window, sinks):
+    _prefill(kpa(), SPLITS[name], fmt, 64, past, new, window, sinks, 67)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
 def test_decode(name, fmt):
     _decode(kpa(), SPLITS[name], fmt, 32, [1, 77, 0, 301, 16, 1000], 0, 0, 20)
 
