@@ -16,9 +16,9 @@
 // Kronecker product's factors multiply), its two value scales its B^V in fp16, times 2^8 that
 // the output takes back, so codes near 448 and usual magnitudes both sit well inside fp16.
 //
-// Data movement: 16-slot groups are contiguous in the pool, so each is one cp.async.bulk per
-// plane through the page table into a ring of STAGES tiles; the last warp to release a stage
-// issues its next tile.  The table entries of that tile are fetched while the current one is
+// Data movement: 16-slot groups are contiguous in the pool, so a run of them that the page table
+// leaves together is one cp.async.bulk per plane into a ring of STAGES tiles; the last warp to
+// release a stage issues its next tile, all warps the first ring.  The table entries of that tile are fetched while the current one is
 // computed.  Only groups with a visible slot are copied; the slots of such a group that the
 // query does not see are masked in the scores and zeroed in the value operands, so their
 // bytes may hold anything.  Waits are bounded.
@@ -76,8 +76,9 @@ struct Cfg {
     static constexpr size_t SMEM = OFF_FLAGS + 4 * (1 + STAGES);
     static_assert(MA % (16 * HS) == 0 && (KPA || (D1 == 1 && H2 == 1)) && (!KPA || HS == 1), "shape");
     static_assert(D2 % 16 == 0 || (KPA && D2 == 8), "d2");
-    static constexpr int FIRST = (STAGES * TG + 31) / 32;          // groups of the first ring per lane of a warp
-    static_assert(WARPS <= 16 && TG <= 32, "one warp issues a tile");
+    static constexpr int OFF_V = TG * KG;                          // a stage: the tile's K groups, then its V groups
+    static constexpr int FIRST = (STAGES * TG + WARPS - 1) / WARPS;           // groups of the first ring per warp
+    static_assert(WARPS <= 16 && TG <= 32 && FIRST <= 32, "one warp issues a tile");
     static_assert((size_t)(SLICES * H * (MO_LD + 2) + H * (DH + 2)) * 4 <= (size_t)STAGES * STAGE_BYTES,
                   "slice merge and merged partial fit in the ring");
     static_assert(SMEM <= 226 * 1024, "shared memory (a little is static)");
@@ -248,16 +249,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     // without a window the first ring's table entries do not depend on the length: fetch them
     // beside it (inside the row for every slot below max_len)
     const int v0 = split * gps;
-    int first_page[C::FIRST], first_in[C::FIRST];
-    const bool early = a.p.mask.window == 0;
-#pragma unroll
-    for (int k = 0; k < C::FIRST; ++k) {
-        const int i = lane + 32 * k;
-        if (warp == 0 && early && i < STAGES * TG && (long long)(v0 + i) * 16 < a.p.max_len) {
-            int entry;
-            split_group(a.pool, v0 + i, entry, first_in[k]);
-            first_page[k] = __ldg(trow + entry);
-        }
+    int first_page = 0, first_in = 0;
+    const bool early = a.p.mask.window == 0, first_ring = lane < C::FIRST && warp * C::FIRST + lane < STAGES * TG;
+    const int first_group = v0 + warp * C::FIRST + lane;
+    if (first_ring && early && (long long)first_group * 16 < a.p.max_len) {
+        int entry;
+        split_group(a.pool, first_group, entry, first_in);
+        first_page = __ldg(trow + entry);
     }
     // query fragments (A operand): row g (g + 8) of tile mt is (i1, j1) = (2 mt + (g >> 2), 2 (g & 3)) and
     // (i1, j1 + 1) with d1 = 8, head 16 mt + g (+ 8) with d1 = 1
@@ -354,27 +352,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         }
         return (size_t)page * a.pool.pg + in;
     };
-    auto copy_group = [&](int stage, int i, size_t group) {
-        const uint32_t dst = smem_u32(smem) + stage * C::STAGE_BYTES + i * (KG + VG);
-        bulk_g2s(dst, a.pool.k + group * KG, KG, full0 + 8 * stage);
-        bulk_g2s(dst + KG, a.pool.v + group * VG, VG, full0 + 8 * stage);
+    // Each lane's group (has) into place `at` of a stage, by a whole warp whose lanes hold places in order.
+    // Groups that follow one another in the pool go as one copy per plane: a warp issues its lanes' copies
+    // one after the other, about 100 clocks each.
+    auto copy_groups = [&](int stage, int at, bool has, size_t group) {
+        const size_t before = __shfl_up_sync(0xffffffffu, (unsigned long long)group, 1);
+        const uint32_t heads = __ballot_sync(0xffffffffu, !has || lane == 0 || at == 0 || group != before + 1);
+        if (has && (heads >> lane & 1u)) {
+            const uint32_t later = lane == 31 ? 0u : heads >> (lane + 1);
+            const uint32_t len = later ? __ffs(later) : 32 - lane;
+            const uint32_t dst = smem_u32(smem) + stage * C::STAGE_BYTES;
+            bulk_g2s(dst + at * KG, a.pool.k + group * KG, len * KG, full0 + 8 * stage);
+            bulk_g2s(dst + C::OFF_V + at * VG, a.pool.v + group * VG, len * VG, full0 + 8 * stage);
+        }
+        __syncwarp();
     };
     auto groups_in = [&](int t) { return min(TG, v1 - v0 - t * TG); };
-    if (warp == 0) {                                       // the first ring, a lane per group
-        if (lane < STAGES && lane < n_tiles) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < C::FIRST; ++k) {
-            const int i = lane + 32 * k;
-            if (i < STAGES * TG && v0 + i < v1) {
-                if (!early) {
-                    int entry;
-                    split_group(a.pool, tl.slot_tile(v0 + i), entry, first_in[k]);
-                    first_page[k] = __ldg(trow + entry);
-                }
-                copy_group(i / TG, i % TG, group_index(first_page[k], first_in[k]));
-            }
+    if (warp == 0 && lane < STAGES && lane < n_tiles) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
+    {                                                      // the first ring, some groups per warp
+        const bool has = first_ring && first_group < v1;
+        if (has && !early) {
+            int entry;
+            split_group(a.pool, tl.slot_tile(first_group), entry, first_in);
+            first_page = __ldg(trow + entry);
         }
+        const int i = warp * C::FIRST + lane;
+        copy_groups(i / TG, i % TG, has, has ? group_index(first_page, first_in) : 0);
     }
 
     float o[MT][NT][4];
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             float2 sc[NC][MT][HR][2];
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc) {
-                const uint32_t kgrp = stage + (gi0 + cc) * (KG + VG);
+                const uint32_t kgrp = stage + (gi0 + cc) * KG;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             for (int cc = 0; cc < NC; ++cc) {
                 float2 ts[2] = {make_float2(a.p.qscale, a.p.qscale), make_float2(a.p.qscale, a.p.qscale)};
                 if constexpr (Q8) {
-                    const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * (KG + VG) + C::EK * 16 + 4 * c;
+                    const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * KG + C::EK * 16 + 4 * c;
                     const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
                     // bytes: slots 2c, 2c + 8, 2c + 1, 2c + 9
                     ts[0] = make_float2(exp_sum(s4 & 255u) * a.p.qscale, exp_sum((s4 >> 16) & 255u) * a.p.qscale);
@@ -613,10 +616,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             // ---- values
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc) {
-                const uint32_t vgrp = stage + (gi0 + cc) * (KG + VG) + KG;
+                const uint32_t vgrp = stage + C::OFF_V + (gi0 + cc) * VG;
                 uint32_t vs[2] = {0, 0}, p2[MT][HR][2];
                 if constexpr (Q8) {
-                    const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * (KG + VG) + KG + C::EV * 16 + 4 * c;
+                    const unsigned char *e = smem + s * C::STAGE_BYTES + C::OFF_V + (gi0 + cc) * VG + C::EV * 16 + 4 * c;
                     const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
                     // 2^8 times the scales go to B; what would take B below 2^-16 goes to the weights instead
                     // (values near 2^-30 and less: rarely, and for the whole warp at once)
@@ -759,11 +762,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();                                       // lane 0's acquire covers the warp
         if (last) {
-            if (lane < groups_in(t + STAGES)) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                copy_group(s, lane, tab[s * TG + lane]);
-            }
-            __syncwarp();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const int n = groups_in(t + STAGES);
+            copy_groups(s, lane, lane < n, lane < n ? tab[s * TG + lane] : 0);
         }
         if (flags[0]) { aborted = true; break; }
     }
@@ -843,7 +844,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     if (a.cluster) join_cluster();
 }
 
-// (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools)
+// (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools).
+// Blocks are as large as an SM holds: smaller ones start sooner on short sequences and lose more on long
+// ones (variant 0, bf16, 4 slices and 3 stages against 8 and 2: 8 x 4096 tokens 9.9 us against 11.2,
+// 64 x 4096 51 against 45, 4 x 65536 55 against 35; variant 4, e4m3, 2 slices of 4 chunks against 8 of 2:
+// 64 x 4096 25.2 against 24.7, 65536 36.9 against 16.8).
 #define KPA_PAGED_DECODE_VARIANTS(X)            \
     X(0, 16, 1, 64, 2, 2, 1, 1, 8, 1, 2, 8, 2, 2)    \
     X(1, 32, 8, 16, 4, 4, 8, 1, 2, 1, 2, 2, 2, 2)    \
