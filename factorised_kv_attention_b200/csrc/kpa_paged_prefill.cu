@@ -429,24 +429,26 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             // step i of half hh
             auto issue_s = [&](int hh, int i) -> bool {
                 const int t = tp.tile(hh, i), kb = tp.k_buf(t);
-                if (!wait(B_K_FULL + kb, tp.k_use(t) & 1)) return false;
-                tc_fence_after();
                 const uint32_t q_lo = tp.alt ? d_q : d_q + hh * (C::Q_HALF >> 4), k_lo = d_0 + (k_off(t) >> 4);
                 const uint32_t s_addr = tmem + hh * 128;
+                const bool last = tp.last_half(hh, i);
+                if (!wait(B_K_FULL + kb, tp.k_use(t) & 1)) return false;
+                tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < DH / 16; ++k)
                     umma_ss(s_addr, q_lo + (k / 4) * (HQ * 128 >> 4) + 2 * (k % 4), k_lo + (k / 4) * (TK * 128 >> 4) + 2 * (k % 4),
                             idesc_s, k > 0);
                 umma_commit(bar(B_S_FULL + hh));
-                if (tp.last_half(hh, i)) umma_commit(bar(B_K_EMPTY + kb));
+                if (last) umma_commit(bar(B_K_EMPTY + kb));
                 return true;
             };
             auto issue_pv = [&](int hh, int i) -> bool {
                 const int t = tp.tile(hh, i), vb = tp.v_buf(t);
-                if (!wait(B_P_HALF + hh, i & 1)) return false;
-                if (tp.first_half(hh, i) && !wait(B_V_FULL + vb, tp.v_use(t) & 1)) return false;
-                tc_fence_after();
                 const uint32_t v_lo = d_0 + (v_off(t) >> 4);
+                const bool first = tp.first_half(hh, i), last = tp.last_half(hh, i), final = i == tp.steps(hh) - 1;
+                if (!wait(B_P_HALF + hh, i & 1)) return false;
+                if (first && !wait(B_V_FULL + vb, tp.v_use(t) & 1)) return false;
+                tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k) {
                     if (k == TK / 32) {                               // the rest of P
@@ -456,8 +458,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     umma_ts_lo(tmem + 256 + hh * 128, tmem + hh * 128 + 8 * k, v_lo + (k / 4) * (DH * 128 >> 4) + 2 * (k % 4), idesc_o,
                                i > 0 || k > 0);
                 }
-                if (tp.last_half(hh, i)) umma_commit(bar(B_V_EMPTY + vb));
-                if (i == tp.steps(hh) - 1) umma_commit(bar(B_O_FINAL + hh));
+                if (last) umma_commit(bar(B_V_EMPTY + vb));
+                if (final) umma_commit(bar(B_O_FINAL + hh));
                 return true;
             };
 #pragma unroll
