@@ -5,16 +5,15 @@
 //
 // The arrangement is the contiguous cache's prefill: one CTA takes 256 query rows of one
 // (sequence, head) as two 128-row halves that share every rebuilt 128-slot K/V tile and take
-// turns on the tensor pipe; a producer warp per plane streams factor slices with TMA, eight warps
+// turns on the tensor pipe; a producer warp per plane streams factor slices, eight warps
 // rebuild K and V^T as fp16 in the 128-byte-swizzled layouts tcgen05.mma reads, one thread
 // issues S_h = Q_h K^T and O_h += P_h V, and eight softmax warps (a row per thread) turn S_h
 // into P_h in tensor memory (S0 | S1 | O0 | O1, 128 columns each).  What differs:
 //   - rows come flattened, each CTA finds its sequence by a scan of the row offsets;
 //   - the tiles are those the CTA's rows see: the sinks' and the windows', or one of n_split
 //     equal runs of them when there are few CTAs, whose partials a second kernel joins;
-//   - a tile's 16-slot groups come through the page table: the producer's lanes each load
-//     boxes of as many groups as a page surely holds together (1, 2, 4 or 8), and skip boxes
-//     that no row sees; rebuilt slots that no row sees are zeros;
+//   - a tile's 16-slot groups come through the page table as 16-byte asynchronous copies;
+//     groups that no row sees are skipped, rebuilt slots that no row sees are zeros;
 //   - a CTA with at most 128 rows has both halves work on them, on tiles in turns, each with
 //     its own maxima, sums and output, joined at the end: a tile then costs its rebuild and not
 //     the chain of a half's products and softmax (9 x 128 rows over 4096 slots, 4 x 4 heads of
@@ -59,7 +58,6 @@ struct PrefillArgsP {
     PagedAttnArgs p;
     Pool pool;
     int h1, h2;
-    int box_groups;                           // 16-slot groups per TMA box: 1, 2, 4 or 8
     unsigned long long wait_limit_ns;
 };
 
@@ -174,8 +172,7 @@ struct TilePlan {
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgsP a) {
+paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ PrefillArgsP a) {
     constexpr int D1 = C::D1, R = C::R, DH = C::DH;
     [[maybe_unused]] constexpr int HB = C::HB;
     constexpr bool E4M3 = C::E4M3;
@@ -188,11 +185,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        tma_prefetch_desc(&tmq);
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
-    }
+    if (tid == 0) tma_prefetch_desc(&tmq);
     const int head = blockIdx.x, split = blockIdx.y;                // (the parts of the longest tiles start first)
     const int h = a.h1 * a.h2, i1 = head / a.h2, i2 = head % a.h2;
     const uint64_t limit = a.wait_limit_ns;
@@ -240,54 +233,29 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
 
     // ---- producers' side (one warp per plane): page lookups and copies
     const bool is_producer = warp >= kProducerWarp, prod_v = warp == kProducerWarp + 1;
-    const int bg = a.box_groups, nb = TK / 16 / bg;               // boxes of a tile
-    const int rows = E4M3 ? bg : 2 * bg;                          // layout groups of a box
-    // Pages are looked up for 32 runs of slots at a time (a load waited for at every unit would cost the
-    // warp more than its copies): lane l holds run l % n_runs of unit u + l / n_runs.  A run is a box at
-    // d1 = 8, a group of the unit at d1 = 1.  in_page: its first 16-slot group inside its page (-1: nothing,
-    // or seen by no row).
-    const int n_runs = C::TPA ? C::NG : nb, units = 32 / n_runs;          // (powers of two)
+    // Pages are looked up for several units at a time (a load waited for at every unit would cost the warp
+    // more than its copies): lane l holds run l % RUNS of unit u + l / RUNS.  A run is 16 slots at d1 = 8, a
+    // group of the unit at d1 = 1.  in_page: its 16-slot group inside its page (-1: nothing, or seen by no
+    // row).
+    constexpr int RUNS = C::TPA ? C::NG : TK / 16, UNITS = 32 / RUNS;
     int page = 0, in_page = -1;
     auto fetch = [&](int u0) {
         in_page = -1;
-        const int u = u0 + lane / n_runs, t = u / C::NU;
+        const int u = u0 + lane / RUNS, t = u / C::NU;
         if (t >= tp.n_kt) return;
-        const int span = C::TPA ? (E4M3 ? 16 : 8) : bg * 16;
-        const int s0 = tl.slot_tile(v0 + t) * TK + (u % C::NU) * C::US + lane % n_runs * span;
+        constexpr int span = C::TPA && !E4M3 ? 8 : 16;
+        const int s0 = tl.slot_tile(v0 + t) * TK + (u % C::NU) * C::US + lane % RUNS * span;
         if (s0 > hi || (s0 + span <= wstart && s0 >= a.p.mask.sinks)) return;
         int entry;
         split_group(a.pool, s0 >> 4, entry, in_page);
         page = __ldg(a.pool.table + (size_t)b * a.pool.table_stride + entry);
     };
-    // copies of this lane: box (lane + 32 j) % nb of block (lane + 32 j) / nb
-    // (d1 = 1: the lane's group's B rows, and one A row of group lane / R: byte offsets in a 16-slot group)
-    constexpr int CP = C::TPA ? 1 : (C::NBLK * 8 + 31) / 32;
-    int cp_x[CP], cp_dst[CP], cp_box[CP];
-    auto plan_copies = [&] {
-        const int ab = R * a.h1 * D1;                             // first B element of a record
-        if constexpr (C::TPA) {
-            const int half = (prod_v ? a.pool.vg : a.pool.kg) / 2;        // of the two 8-slot groups of a bf16 one
-            cp_x[0] = ab * 16 + (!E4M3 && (lane & 1) ? half : 0);
-            cp_dst[0] = lane * C::GROUP;
-            cp_box[0] = ((lane % R) * a.h1 + i1) * 16 + (!E4M3 && (lane / R & 1) ? half : 0);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < CP; ++j) {
-            const int i = lane + 32 * j, k = i >> (31 - __clz(nb));       // (nb is a power of two)
-            cp_box[j] = i & (nb - 1);
-            cp_x[j] = k >= C::NBLK ? -1
-                      : 4 * (k < R ? k * a.h1 * D1 + i1 * D1
-                                   : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8);
-            cp_dst[j] = k * C::BOX + cp_box[j] * rows * 128;
-        }
-    };
     // the head's factor slices of unit u (its pages looked up) into its stage, which is free
     auto copy_factors = [&](int u) {
-        const int from = (u & (units - 1)) * n_runs + (lane & (n_runs - 1));
+        const int from = u % UNITS * RUNS + lane % RUNS;
         const int pu = __shfl_sync(0xffffffffu, page, from), iu = __shfl_sync(0xffffffffu, in_page, from);
-        long long grp = -1;                                       // (lane < n_runs) first group of this lane's run
-        if (lane < n_runs && iu >= 0) {
+        long long grp = -1;                                       // (lane < RUNS) the group of this lane's run
+        if (lane < RUNS && iu >= 0) {
             const bool bad = pu < 0 || pu >= a.pool.n_pages;
             if (bad) raise_error(a.p.err, kErrDeviceCheck);
             grp = (long long)(bad ? 0 : pu) * a.pool.pg + iu;
@@ -295,37 +263,47 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const int s = u % C::FST;
         const uint32_t full = bar((prod_v ? B_VST_FULL : B_KST_FULL) + s);
         const uint32_t st = smem_u32(smem + (prod_v ? C::OFF_VST : C::OFF_KST) + (size_t)s * C::ST);
+        const unsigned char *plane = prod_v ? a.pool.v : a.pool.k;
+        const int gb = prod_v ? a.pool.vg : a.pool.kg;
+        const int ab = R * a.h1 * D1;                             // first B element of a record
         if constexpr (C::TPA) {
             // The B rows as one bulk copy per group (each costs its warp about 100 clocks, one lane after the
-            // other), the 16-byte A rows as plain asynchronous copies; every lane arrives for its own.
-            const unsigned char *plane = prod_v ? a.pool.v : a.pool.k;
-            const size_t gbytes = prod_v ? a.pool.vg : a.pool.kg;
+            // other), the 16-byte A rows as plain asynchronous copies.
             const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
             if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * C::GROUP);
             __syncwarp();
-            if (grp >= 0) sm100::bulk_g2s(st + cp_dst[0], plane + (size_t)grp * gbytes + cp_x[0], C::GROUP, full);
+            auto half = [&](int g) { return !E4M3 && (g & 1) ? gb / 2 : 0; };      // of the two 8-slot groups of 16 slots
+            if (grp >= 0) sm100::bulk_g2s(st + lane * C::GROUP, plane + grp * gb + half(lane) + ab * 16, C::GROUP, full);
             const long long ga = __shfl_sync(0xffffffffu, grp, lane / R % C::NG);
-            if (lane < C::NG * R && ga >= 0) sm100::cp_async16(st + C::OFF_A + lane * 16, plane + (size_t)ga * gbytes + cp_box[0]);
-            sm100::cp_async_arrive(full);
-            return;
-        }
-        const int loaded = __popc(__ballot_sync(0xffffffffu, grp >= 0));
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)loaded * (C::NBLK * rows * 128 + (E4M3 ? bg * 32 : 0)));
-        __syncwarp();
-        const CUtensorMap *map = prod_v ? &tmv : &tmk;
+            if (lane < C::NG * R && ga >= 0)
+                sm100::cp_async16(st + C::OFF_A + lane * 16,
+                                  plane + ga * gb + half(lane / R) + ((lane % R) * a.h1 + i1) * 16);
+        } else {
+            // Runs of 8 rows of 16 bytes, four groups at a time: plain asynchronous copies, 24 instructions a
+            // plane and tile at R = 2 in bf16 whatever the page size (a tensor copy per page and run costs the
+            // warp about 130 clocks each: 96 of them at R = 4 and 16-slot pages).
+            const int row = lane & 7;
+#pragma unroll 1
+            for (int g0 = 0; g0 < C::NG; g0 += 4) {
+                const int g = g0 + (lane >> 3);
+                const long long gg = __shfl_sync(0xffffffffu, grp, E4M3 ? g : g >> 1);
+                const unsigned char *src = plane + gg * gb + (!E4M3 && (g & 1) ? gb / 2 : 0) + row * 16;
+                const uint32_t dst = st + g * 128 + row * 16;
+                if (gg >= 0) {
 #pragma unroll
-        for (int j = 0; j < CP; ++j) {
-            const long long g = __shfl_sync(0xffffffffu, grp, cp_box[j]);
-            if (g >= 0 && cp_x[j] >= 0) tma_load_2d(st + cp_dst[j], map, cp_x[j], (int)(E4M3 ? g : 2 * g), full);
-        }
-        if constexpr (E4M3) {                                     // the two scale rows of each group
-            const long long g = __shfl_sync(0xffffffffu, grp, (lane & 7) / bg);
-            if (lane < 8 && g >= 0) {
-                const int gb = prod_v ? a.pool.vg : a.pool.kg;
-                const unsigned char *src = (prod_v ? a.pool.v : a.pool.k) + (size_t)(g + lane % bg) * gb + gb - 32;
-                sm100::bulk_g2s(st + C::FACT + lane * 32, src, 32, full);
+                    for (int k = 0; k < C::NBLK; ++k) {
+                        const int e = k < R ? (k * a.h1 + i1) * D1
+                                            : ab + (((k - R) / HB) * a.h2 + i2) * C::D2 + ((k - R) % HB) * 8;
+                        sm100::cp_async16(dst + k * C::BOX, src + e * 16);
+                    }
+                }
+            }
+            if constexpr (E4M3) {                                 // the two scale rows of each group
+                const long long gg = __shfl_sync(0xffffffffu, grp, lane >> 1 & 7);
+                if (lane < 16 && gg >= 0) sm100::cp_async16(st + C::FACT + lane * 16, plane + gg * gb + gb - 32 + (lane & 1) * 16);
             }
         }
+        sm100::cp_async_arrive(full);                             // every lane, for its own copies
     };
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -338,7 +316,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             for (int i = 0; i < C::NBAR; ++i) {
                 uint32_t count = 1;
                 if ((i >= B_QREADY && i < B_QREADY + 2) || (i >= B_P_HALF && i < B_P_FULL + 2)) count = 4;
-                if (C::TPA && i >= B_KST_FULL && i < B_KST_EMPTY) count = 1 + 32;
+                if (i >= B_KST_FULL && i < B_KST_EMPTY) count = C::TPA ? 1 + 32 : 32;
                 if (i >= B_KST_EMPTY || (i >= B_K_FULL && i < B_K_FULL + 2) || (i >= B_V_FULL && i < B_V_FULL + 2)) count = C::TPA ? kRebuildWarps / 2 : kRebuildWarps;
                 mbar_init(bar(i), count);
             }
@@ -357,7 +335,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         }
         __syncwarp();
     }
-    if (is_producer) plan_copies();
     if (warp == kProducerWarp && tp.n_kt > 0) copy_factors(0);
     tc_fence_before();
     __syncthreads();
@@ -407,7 +384,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             if (prod_v) copy_factors(0);
             int issued = 0;
             for (int u = 1; u < tp.n_kt * C::NU; ++u) {
-                if ((u & (units - 1)) == 0) fetch(u);
+                if (u % UNITS == 0) fetch(u);
                 if (u >= C::FST && !wait_warp(b_empty + u % C::FST, ((u / C::FST) - 1) & 1)) break;
                 copy_factors(u);
                 issued = u;
@@ -982,20 +959,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     }
 }
 
-// A pool plane viewed as [groups][E rows] of 16 bytes (32-bit elements): boxes of 8 rows x
-// `rows` groups, no swizzle.
-bool make_plane_map(CUtensorMap *map, const void *plane, uint64_t groups, uint64_t group_bytes, int rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {group_bytes / 4, groups};
-    cuuint64_t strides[1] = {group_bytes};
-    cuuint32_t box[2] = {32, (cuuint32_t)rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void *>(plane), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class C>
 cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned long long wait_limit_ns, cudaStream_t st) {
     PrefillArgsP a;
@@ -1004,19 +967,12 @@ cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned lon
     a.h1 = s.d.h1;
     a.h2 = s.d.h2;
     a.wait_limit_ns = wait_limit_ns;
-    a.box_groups = 8;                            // as many groups as every aligned run of them shares a page
-    while (s.pool.pg % a.box_groups != 0) a.box_groups /= 2;
-    CUtensorMap tmq, tmk, tmv;                   // (the planes' unused, but prefetched, at d1 = 1)
-    const uint64_t sub = C::E4M3 ? 1 : 2, groups = (uint64_t)s.pool.n_pages * s.pool.pg * sub;
-    const int rows = a.box_groups * (int)sub;
-    if (!make_q_map(&tmq, p.q, (uint64_t)p.n_rows, (uint64_t)s.d.h * s.d.dh, HQ) ||
-        !make_plane_map(&tmk, s.pool.k, groups, (uint64_t)s.pool.kg / sub, rows) ||
-        !make_plane_map(&tmv, s.pool.v, groups, (uint64_t)s.pool.vg / sub, rows))
-        return cudaErrorInvalidValue;
+    CUtensorMap tmq;
+    if (!make_q_map(&tmq, p.q, (uint64_t)p.n_rows, (uint64_t)s.d.h * s.d.dh, HQ)) return cudaErrorInvalidValue;
     cudaError_t e = ensure_dynamic_smem<paged_prefill_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)(((long long)p.n_rows + (long long)p.batch * (2 * HQ - 1)) / (2 * HQ));
-    paged_prefill_kernel<C><<<dim3((unsigned)s.d.h, (unsigned)p.n_split, tiles), kThreads, C::SMEM, st>>>(tmq, tmk, tmv, a);
+    paged_prefill_kernel<C><<<dim3((unsigned)s.d.h, (unsigned)p.n_split, tiles), kThreads, C::SMEM, st>>>(tmq, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.n_split == 1) return e;
     return launch_paged_combine(s, p, st);
@@ -1028,8 +984,7 @@ int paged_prefill_rows() { return 2 * HQ; }
 
 bool paged_prefill_supported(const PagedShape &s) {
     const Dims &d = s.d;
-    // group coordinates of the tensor maps are 32-bit
-    if ((uint64_t)s.pool.n_pages * s.pool.pg * 2 > INT32_MAX || d.rk != d.rv) return false;
+    if (d.rk != d.rv) return false;
     if (d.d1 == 1) return d.h2 == 1 && ((d.d2 == 64 && d.rk <= 2) || (d.d2 == 128 && d.rk == 2));
     return d.d1 == 8 && ((d.d2 == 16 && (d.rk == 2 || d.rk == 4)) || (d.d2 == 8 && d.rk == 2));
 }
