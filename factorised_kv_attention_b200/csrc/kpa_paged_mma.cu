@@ -14,6 +14,8 @@
 //   - each warp forms S = Q K^T for its 16 rows on m16n8k16 (fp16 operands, fp32 sums),
 //     masks it, runs the online softmax in registers and adds P V (P rounded to fp16, 2^-11
 //     relative) into its fp32 output tile.
+// Bound by the rebuild and its fragments' way through shared memory: 8 x 2048 causal tokens of
+// 4 x 4 heads of 8 x 16, R = 2, in 1179 us (117 TFLOP/s), where the tcgen05 kernel takes 255.
 #include <cuda_fp16.h>
 
 #include "kpa_f32x2.cuh"

@@ -10,7 +10,9 @@
 // of all 16 slots: a warp reads (writes) 128 contiguous bytes of each record and writes
 // (reads) whole 16-byte rows of the group, and the transposition is the thread's registers.
 // Nothing goes through shared memory but the rotation table and the largest magnitudes of
-// the 16 tokens.  Bound by latency at a few tokens and by memory beyond.
+// the 16 tokens.  Bound by latency at a few tokens (4.4 us for 48) and by issue slots beyond:
+// 16384 tokens of 384 values written as e4m3 in 12.0 us (1.6 TB/s; 66 % of the issue slots), 16384
+// of 576 read back in 9.5 us (3.0 TB/s).
 #include <string.h>
 
 #include <algorithm>
