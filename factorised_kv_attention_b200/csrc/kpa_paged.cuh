@@ -49,7 +49,8 @@ struct Tiles {
 __device__ __forceinline__ Tiles visible_tiles(const Mask &m, int lo, int hi, int T) {
     Tiles t;
     const int first = window_start(m, lo) / T, last = hi / T;
-    const int sink_tiles = m.window > 0 ? (min(m.sinks, hi + 1) + T - 1) / T : 0;
+    const int sink_slots = m.window > 0 ? min(m.sinks, hi + 1) : 0;
+    const int sink_tiles = sink_slots > 0 ? (sink_slots - 1) / T + 1 : 0;        // (sinks up to INT_MAX)
     t.head = min(sink_tiles, first);
     t.gap = first - t.head;
     t.n = t.head + (last - first + 1);
@@ -280,7 +281,7 @@ int paged_mma_rows();                                        // rows of a tile
 cudaError_t launch_paged_mma(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedShape &s, const PagedAttnArgs &a, cudaStream_t st);
 
-// The tcgen05 chunk kernel (d1 = 8): whether it takes this shape and pool, and its launcher.
+// The tcgen05 chunk kernel: whether it takes this shape and pool, and its launcher.
 bool paged_prefill_supported(const PagedShape &s);
 int paged_prefill_rows();                                    // rows of a tile
 cudaError_t launch_paged_prefill(const PagedShape &s, const PagedAttnArgs &a, unsigned long long wait_limit_ns,

@@ -138,7 +138,7 @@ kpa_status check_attn(const kpa_config *cfg, const kpa_pages *pg, int32_t batch,
     if ((int64_t)max_len > (int64_t)pg->page_size * pg->table_stride) return KPA_ERR_INVALID_ARG;
     if (st != KPA_OK) return st;
     if (!paged_mma_supported(s->d, s->pool.e4m3 != 0)) return KPA_ERR_UNSUPPORTED;
-    // row tiles (of chunks) and sequences (single tokens) are blocks in y
+    // row tiles (of chunks) and sequences (single tokens) are blocks in y or z
     if (batch > 65535 || (chunks && n_rows / paged_mma_rows() + (int64_t)batch > 65535)) return KPA_ERR_UNSUPPORTED;
     return KPA_OK;
 }

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const MmaArgs a)
 
         // no row of the warp sees the tile
         if (!warp_live || t0 > warp_hi ||
-            (t0 + kSlots <= window_start(a.p.mask, warp_lo) && t0 >= a.p.mask.sinks && a.p.mask.window > 0))
+            (t0 + kSlots - 1 < window_start(a.p.mask, warp_lo) && t0 >= a.p.mask.sinks && a.p.mask.window > 0))
             continue;
         // ---- S = Q K^T (16 rows x 64 slots)
         float s[8][4];

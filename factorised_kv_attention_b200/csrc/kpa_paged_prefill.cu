@@ -1,6 +1,6 @@
 // kpa_paged_prefill.cu -- attention of chunks of new tokens over a paged factor cache on the
-// tcgen05 tensor cores, for d1 = 8 (d2 = 16 at R = 2 or 4, d2 = 8 at R = 2) and d1 = 1, TPA's
-// split (d2 = 64 at R = 1 or 2, d2 = 128 at R = 2); every other split runs on the mma.sync
+// tcgen05 tensor cores, for d1 = 8 (d2 = 16 at R = 2 or 4, d2 = 8 at R = 2) and d1 =
+// h2 = 1, TPA's split (d2 = 64 at R = 1 or 2, d2 = 128 at R = 2); every other split runs on the mma.sync
 // kernel.
 //
 // The arrangement is the contiguous cache's prefill: one CTA takes 256 query rows of one

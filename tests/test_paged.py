@@ -303,6 +303,17 @@ def test_decode_large_batch(fmt):
     _decode(kpa(), SPLITS["kpa_4x4_8x16_r2"], fmt, 16, [int(x) for x in rng.integers(0, 200, 333)], 90, 2, 24)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_several_b_heads_at_d1_one(fmt):
+    """A split of TPA's d1 and d2 whose B factors are not shared by every head."""
+    s = Shape(h1=8, h2=2, d1=1, d2=64, r_k=2, r_v=2)
+    cfg, pages = kpa().make_config(s, "bf16"), kpa().make_pages(32, 1, 1, fmt)
+    assert kpa().kpa_paged_prefill_kernel_kind(cfg, pages) == "chunks"
+    _prefill(kpa(), s, fmt, 32, [0, 77, 300], [130, 1, 40], 0, 0, 68)
+    _prefill(kpa(), s, fmt, 48, [290, 64], [3, 260], 100, 20, 69)
+    _decode(kpa(), s, fmt, 32, [1, 77, 0, 301], 0, 0, 70)
+
+
 @pytest.mark.parametrize("name", ["kpa_4x4_8x16_r2", "tpa_16_64_r2", "kpa_3x2_4x6_r2"])
 def test_prefill_many_sequences(name):
     """More sequences than the ordered search of a row tile holds."""
