@@ -79,7 +79,7 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         int64_t per = (tiles + per_seq - 1) / per_seq;
         const int64_t wave = (int64_t)sms * per_sm;
         // Long batches: the lengths, which are not known here, may differ, so the blocks size the splits (32
-        // sequences of 1024 .. 8192 tokens, R = 4: 79 us, splits sized from the longest 91).  Short ones do
+        // sequences of 1024 .. 8192 tokens, R = 4: 82 us, splits sized from the longest 91).  Short ones do
         // not repay the search.
         if (batch > 1 && batch <= kPagedMaxSlotSeqs && (per >= 16 || per_seq == 1) && tiles >= 8) {
             p.n_slots = (int)(wave * std::min<int64_t>(4, (3 * (int64_t)batch + wave - 1) / wave));
