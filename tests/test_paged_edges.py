@@ -7,8 +7,7 @@ import torch
 import paged_marks as pm
 import paged_util as pu
 from gpu_util import kpa
-from test_paged import FORMATS, _append, _check_records, _cu, _i32, _no_error
-from test_paged_ranges import SPLITS
+from test_paged import FORMATS, SPLITS, _append, _check_records, _cu, _i32, _no_error
 from workloads import Shape
 
 pytestmark = pytest.mark.gpu
