@@ -256,6 +256,10 @@ Dims config_dims(const kpa_config *cfg) { return dims_of(cfg); }
 RopeTable config_rope(const kpa_config *cfg) { return rope_table(cfg); }
 kpa_status device_info(int **err, int *sms) { return device_state(err, sms); }
 unsigned long long device_wait_limit_ns() { return current_hooks().wait_limit_ns; }
+void device_skip_hook(int *tile, int *split) {
+    *tile = current_hooks().skip_tile;
+    *split = current_hooks().skip_split;
+}
 
 kpa_status decode_dense_plan(const kpa_config *cfg, int batch, int max_len, size_t *total, size_t *offset,
                              size_t *bytes) {

@@ -105,12 +105,13 @@ void record_cuda_error(cudaError_t e);
 
 // Shared by the entry points of every file: the shape checks of a config, its derived
 // sizes and RoPE frequencies, the current device's error word and SM count, and the
-// calling thread's bound on device waits.
+// calling thread's bound on device waits and the tile whose copy a test withholds (-1: none).
 kpa_status config_check(const kpa_config *cfg);
 Dims config_dims(const kpa_config *cfg);
 RopeTable config_rope(const kpa_config *cfg);
 kpa_status device_info(int **err, int *sms);
 unsigned long long device_wait_limit_ns();
+void device_skip_hook(int *tile, int *split);
 
 // ---- host-side launchers (one per kernel file) ------------------------------
 // pos_offset (nullable, device [batch]): the keys of slot s are rotated at position

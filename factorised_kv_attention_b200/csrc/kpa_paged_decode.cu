@@ -56,6 +56,7 @@ struct DecodeArgsP {
     int n_slots;                  // blocks, with p.slots
     int cluster;                  // the splits of a sequence are one cluster and merge over shared memory
     unsigned long long limit_ns;
+    int skip_tile, skip_split;    // (tests) a tile of a split of sequence 0 that is never copied, or -1
 };
 
 // MA = h1*d1 rows of the products of one i2, SLICES token slices per CTA, HS warps that share
@@ -76,8 +77,9 @@ struct Cfg {
     static constexpr int MO_LD = DH + 8;                           // padded rows of the slice merge
     static constexpr size_t OFF_BARS = (size_t)STAGES * STAGE_BYTES;
     static constexpr size_t OFF_TAB = OFF_BARS + 8 * STAGES;                         // group indices of the next tiles
-    static constexpr size_t OFF_FLAGS = OFF_TAB + 8 * STAGES * TG;                   // [0] abort, [1 + s] releases
-    static constexpr size_t SMEM = OFF_FLAGS + 4 * (1 + STAGES);
+    // [0] abort, [1 + s] releases of stage s, [1 + STAGES + s] the last tile issued into it
+    static constexpr size_t OFF_FLAGS = OFF_TAB + 8 * STAGES * TG;
+    static constexpr size_t SMEM = OFF_FLAGS + 4 * (1 + 2 * STAGES);
     static_assert(MA % (16 * HS) == 0 && (KPA || (D1 == 1 && H2 == 1)) && (!KPA || HS == 1), "shape");
     static_assert(D2 % 16 == 0 || (KPA && D2 == 8), "d2");
     static constexpr int OFF_V = TG * KG;                          // a stage: the tile's K groups, then its V groups
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(full0 + 8 * s, 1);
         for (int i = 0; i < 1 + STAGES; ++i) flags[i] = 0;
+        for (int s = 0; s < STAGES; ++s) flags[1 + STAGES + s] = s;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -372,9 +375,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         __syncwarp();
     };
     auto groups_in = [&](int t) { return min(TG, v1 - v0 - t * TG); };
-    if (warp == 0 && lane < STAGES && lane < n_tiles) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
+    auto withheld = [&](int t) { return t == a.skip_tile && split == a.skip_split && b == 0; };
+    if (warp == 0 && lane < STAGES && lane < n_tiles && !withheld(lane)) mbar_expect_tx(full0 + 8 * lane, groups_in(lane) * (KG + VG));
     {                                                      // the first ring, some groups per warp
-        const bool has = first_ring && first_group < v1;
+        const bool has = first_ring && first_group < v1 && !withheld((warp * C::FIRST + lane) / TG);
         if (has && !early) {
             int entry;
             split_group(a.pool, tl.slot_tile(first_group), entry, first_in);
@@ -420,8 +424,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             split_group(a.pool, tl.slot_tile(v0 + (t + STAGES) * TG + lane), entry, next_in);
             next_page = __ldg(trow + entry);
         }
-        if (!mbar_wait(full0 + 8 * s, (t / STAGES) & 1, a.limit_ns)) {
-            raise_error(a.p.err, kErrTimeout);
+        // (a vote: a warp whose lanes differ, as the time runs out, must not part)
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, (t / STAGES) & 1, a.limit_ns))) {
+            if (lane == 0) raise_error(a.p.err, kErrTimeout);
             flags[0] = 1;
             aborted = true;
             break;
@@ -757,8 +762,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                          : "=r"(old)
                          : "r"(smem_u32((const void *)(flags + 1 + s)))
                          : "memory");
-            last = (old + 1) % WARPS == 0 && t + STAGES < n_tiles && !flags[0];
+            last = (old + 1) % WARPS == 0 && t + STAGES < n_tiles && !flags[0] && !withheld(t + STAGES);
             if (last) {
+                flags[1 + STAGES + s] = t + STAGES;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_expect_tx(full0 + 8 * s, groups_in(t + STAGES) * (KG + VG));
             }
@@ -770,13 +776,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             const int n = groups_in(t + STAGES);
             copy_groups(s, lane, lane < n, lane < n ? tab[s * TG + lane] : 0);
         }
-        if (flags[0]) { aborted = true; break; }
+        if (__any_sync(0xffffffffu, flags[0])) { aborted = true; break; }
     }
     __syncthreads();
-    if (aborted || flags[0]) {                              // copies still in flight land before the CTA ends
-        if (tid == 0)
-            for (int t = max(0, n_tiles - STAGES); t < n_tiles; ++t)
-                (void)mbar_wait(full0 + 8 * (t % STAGES), (t / STAGES) & 1, a.limit_ns);
+    // Copies still in flight, of the last tile issued into each stage, land before the CTA ends or its
+    // partial takes the ring's place.
+    if (aborted || flags[0]) {
+        if (tid < STAGES) {
+            const int t = flags[1 + STAGES + tid];
+            if (t < n_tiles && !withheld(t)) (void)mbar_wait(full0 + 8 * tid, (t / STAGES) & 1, a.limit_ns);
+        }
         __syncthreads();
         if (a.p.n_split > 1) empty_partial();               // (the error is reported; peers must not wait)
         return;
@@ -986,6 +995,7 @@ cudaError_t launch_paged_decode(int variant, const PagedShape &s, const PagedAtt
     a.cluster = cluster;
     a.n_slots = n_slots;
     a.limit_ns = wait_limit_ns;
+    device_skip_hook(&a.skip_tile, &a.skip_split);
     cudaError_t e = cudaErrorInvalidValue;
     switch (variant) {
 #define KPA_CASE(IDX, MA, D1, D2, RK, RV, H2, HS, S0, C0, T0, S1, C1, T1)                              \

@@ -475,7 +475,8 @@ kpa_status kpa_decode_noalloc(const kpa_config *cfg, int32_t batch, const void *
                               int32_t capacity, const int32_t *seq_len, int32_t max_len,
                               float sm_scale, float *out, kpa_stream stream);
 
-/* Testing only: make the tensor-core decode's bounded waits observable.
+/* Testing only: make the tensor-core decode's bounded waits observable (kpa_decode and
+ * the paged decode's kernel on the factors).
  * Every bounded wait on the device gives up after wait_limit_ns (default 1 s)
  * and reports KPA_ERR_TIMEOUT; with skip_tile >= 0 the CTA of split
  * `skip_split` of sequence 0 never issues the copy of its tile `skip_tile`, so
