@@ -8,8 +8,11 @@
 //   O_i2[(i1,j1), j2] += sum_{s,r} (p[(i1,i2), s] A^V_r(s)[i1,j1]) B^V_r(s)[i2,j2]
 // One warp takes 16 slots of one i2.  The query is exact in the operand type (bf16 over a
 // bf16 pool, fp16 over an e4m3 one, whose codes are exact in fp16), so the score products
-// run once; p A^V is rounded once to fp16 (2^-11 relative).  Sums, scores and the softmax
-// are fp32.  With d1 = 8 the rows of an m-tile pair up two j1 of one head per lane, so the
+// run once.  p A^V is rounded once by 2^-11 relative: to tf32 over a bf16 pool, whose B^V goes
+// into the product as it is (fp16 operands lose factors of ordinary products but unequal
+// magnitudes; they took 2 to 7 % less time: 8 x 4096 tokens of 4 x 8 heads of 8 x 16, R = 2,
+// 17.2 us against 18.6, 64 x 4096 102 against 106), to fp16 over an e4m3 one.  Sums, scores
+// and the softmax are fp32.  With d1 = 8 the rows of an m-tile pair up two j1 of one head per lane, so the
 // sum over j1 is one add and two shuffles; with d1 = 1 (TPA) rows are heads.
 //
 // An e4m3 token's two key scales multiply its score (one number per token: the scales of a
@@ -139,6 +142,15 @@ __device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, ui
         asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
 }
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// a float whose upper 19 bits, which a tf32 operand is, are x rounded to nearest (2^-11 relative)
+__device__ __forceinline__ uint32_t to_tf32(float x) { return __float_as_uint(x) + 0x1000u; }
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     uint32_t r;
@@ -666,54 +678,70 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                 }
 #pragma unroll
                 for (int r = 0; r < RV; ++r) {
-                    uint32_t pa[MT][4];                            // P' = p A^V_r: (half, rows g / g + 8)
+                    if constexpr (!Q8) {
+                        // P' = p A^V_r as tf32, the bf16 B^V as it is: fp32's exponents, so that factors of any
+                        // magnitudes keep P's 2^-11.  A half's eight slots are the k of one product: slot 2c at
+                        // k = c and slot 2c + 1 at k = c + 4, in both operands.
+                        uint32_t pt[2][MT][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                        for (int rh = 0; rh < 2; ++rh) {
-                            const int j = (r * MT + mt) * 2 + rh, hr = KPA ? 0 : rh;
-                            if constexpr (Q8) {
-                                uint32_t lo, hi;
-                                e4m3_split(ew[0][j], lo, hi);
-                                pa[mt][rh] = hmul2(p2[mt][hr][0], lo);
-                                pa[mt][2 + rh] = hmul2(p2[mt][hr][1], hi);
-                            } else {
-                                const float2 x0 = fmul2(sc[cc][mt][hr][0], unpack_bf16x2(ew[0][j]));
-                                const float2 x1 = fmul2(sc[cc][mt][hr][1], unpack_bf16x2(ew[1][j]));
-                                pa[mt][rh] = pack_h2(x0.x, x0.y);
-                                pa[mt][2 + rh] = pack_h2(x1.x, x1.y);
-                            }
-                            if constexpr (MASKED) {
-                                pa[mt][rh] = mask_pair(pa[mt][rh], keep[0][0], keep[0][1]);
-                                pa[mt][2 + rh] = mask_pair(pa[mt][2 + rh], keep[1][0], keep[1][1]);
-                            }
-                        }
-                    constexpr int STEP = Q8 ? (NT >= 4 ? 4 : 2) : (NT >= 2 ? 2 : 1);   // 8-feature blocks per load
+                            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int n0 = 0; n0 < NT; n0 += STEP) {
-                        uint32_t b0[STEP], b1[STEP];
-                        if constexpr (Q8) {
-                            uint32_t bw[STEP];
-                            ldsm_list<STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
-                                return b_row(r * NT + (NT == 1 ? 0 : n0 + j));
-                            });
+                                for (int rh = 0; rh < 2; ++rh) {
+                                    const float2 x = fmul2(sc[cc][mt][KPA ? 0 : rh][hf], unpack_bf16x2(ew[hf][(r * MT + mt) * 2 + rh]));
+                                    pt[hf][mt][rh] = !MASKED || keep[hf][0] ? to_tf32(x.x) : 0u;
+                                    pt[hf][mt][2 + rh] = !MASKED || keep[hf][1] ? to_tf32(x.y) : 0u;
+                                }
+                        constexpr int STEP = NT >= 2 ? 2 : 1;          // 8-feature blocks per load
 #pragma unroll
-                            for (int k = 0; k < STEP; ++k) {
-                                e4m3_split(bw[k], b0[k], b1[k]);
-                                b0[k] = hmul2(b0[k], vs[0]);
-                                b1[k] = hmul2(b1[k], vs[1]);
-                            }
-                        } else {
+                        for (int n0 = 0; n0 < NT; n0 += STEP) {
                             // matrices (block, half): half 1 lies one 8-slot group further
                             uint32_t bw[2 * STEP];
                             ldsm_list<2 * STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
                                 return b_row(r * NT + n0 + (j >> 1)) + (j & 1) * C::EV;
                             });
 #pragma unroll
-                            for (int k = 0; k < STEP; ++k) {
-                                b0[k] = bf16x2_to_h2(bw[2 * k]);
-                                b1[k] = bf16x2_to_h2(bw[2 * k + 1]);
+                            for (int k = 0; k < STEP; ++k)
+#pragma unroll
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    const uint32_t w = bw[2 * k + hf];
+                                    const uint32_t b0 = !MASKED || keep[hf][0] ? w << 16 : 0u;
+                                    const uint32_t b1 = !MASKED || keep[hf][1] ? w & 0xffff0000u : 0u;
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt) mma_tf32(o[mt][n0 + k], pt[hf][mt], b0, b1);
+                                }
+                        }
+                        continue;
+                    }
+                    uint32_t pa[MT][4];                            // P' = p A^V_r: (half, rows g / g + 8)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int rh = 0; rh < 2; ++rh) {
+                            const int j = (r * MT + mt) * 2 + rh, hr = KPA ? 0 : rh;
+                            uint32_t lo, hi;
+                            e4m3_split(ew[0][j], lo, hi);
+                            pa[mt][rh] = hmul2(p2[mt][hr][0], lo);
+                            pa[mt][2 + rh] = hmul2(p2[mt][hr][1], hi);
+                            if constexpr (MASKED) {
+                                pa[mt][rh] = mask_pair(pa[mt][rh], keep[0][0], keep[0][1]);
+                                pa[mt][2 + rh] = mask_pair(pa[mt][2 + rh], keep[1][0], keep[1][1]);
                             }
+                        }
+                    constexpr int STEP = NT >= 4 ? 4 : 2;          // 8-feature blocks per load
+#pragma unroll
+                    for (int n0 = 0; n0 < NT; n0 += STEP) {
+                        uint32_t b0[STEP], b1[STEP];
+                        uint32_t bw[STEP];
+                        ldsm_list<STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
+                            return b_row(r * NT + (NT == 1 ? 0 : n0 + j));
+                        });
+#pragma unroll
+                        for (int k = 0; k < STEP; ++k) {
+                            e4m3_split(bw[k], b0[k], b1[k]);
+                            b0[k] = hmul2(b0[k], vs[0]);
+                            b1[k] = hmul2(b1[k], vs[1]);
                         }
                         if constexpr (MASKED) {
 #pragma unroll
