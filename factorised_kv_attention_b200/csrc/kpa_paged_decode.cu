@@ -17,7 +17,9 @@
 //
 // An e4m3 token's two key scales multiply its score (one number per token: the scales of a
 // Kronecker product's factors multiply), its two value scales its B^V in fp16, times 2^8 that
-// the output takes back, so codes near 448 and usual magnitudes both sit well inside fp16.
+// the output takes back, as far as codes up to 448 and down to 2^-3 stay exact there, and its
+// weight beyond that: all products up to 2^22, with their precision down to 2^-16 (of the
+// token's largest |A| |B|).
 //
 // Data movement: 16-slot groups are contiguous in the pool, so a run of them that the page table
 // leaves together is one cp.async.bulk per plane into a ring of STAGES tiles; the last warp to
@@ -642,16 +644,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                 if constexpr (Q8) {
                     const unsigned char *e = smem + s * C::STAGE_BYTES + C::OFF_V + (gi0 + cc) * VG + C::EV * 16 + 4 * c;
                     const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
-                    // 2^8 times the scales go to B; what would take B below 2^-16 goes to the weights instead
-                    // (values near 2^-30 and less: rarely, and for the whole warp at once)
+                    // 2^8 times the scales go to B while that is in [2^-18, 2^7] (bytes 102 .. 127): codes up to
+                    // 448 then stay in fp16, and those down to 2^-3 stay exact.  What is beyond goes to the
+                    // weights, for the whole warp at once (factors of standard deviation 2^-6 and less).
                     float2 f[2] = {make_float2(256.f * exp_sum(s4 & 255u), 256.f * exp_sum((s4 >> 16) & 255u)),
                                    make_float2(256.f * exp_sum((s4 >> 8) & 255u), 256.f * exp_sum(s4 >> 24))};
-                    constexpr float kLow = 1.f / 65536.f;
-                    if (__any_sync(0xffffffffu, fminf(fminf(f[0].x, f[0].y), fminf(f[1].x, f[1].y)) < kLow)) {
+                    constexpr float kLow = 0x1p-18f, kHigh = 0x1p7f;
+                    if (__any_sync(0xffffffffu, (((s4 & 0x7f7f7f7fu) + 0x1a1a1a1au) & ~s4 & 0x80808080u) != 0x80808080u)) {
+                        auto within = [&](float x) { return fminf(fmaxf(x, kLow), kHigh); };
+                        auto inverse = [](float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); };   // of a 2^k
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const float2 w = make_float2(fminf(1.f, f[hf].x * 65536.f), fminf(1.f, f[hf].y * 65536.f));
-                            f[hf] = make_float2(fmaxf(f[hf].x, kLow), fmaxf(f[hf].y, kLow));
+                            const float2 in = make_float2(within(f[hf].x), within(f[hf].y));
+                            const float2 w = fmul2(f[hf], make_float2(inverse(in.x), inverse(in.y)));
+                            f[hf] = in;
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

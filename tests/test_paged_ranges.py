@@ -1,5 +1,5 @@
 """Paged attention on the GPU over magnitudes, against the definition in 64 bits: factors whose A
-and B differ by powers of two, and small values."""
+and B differ by powers of two, values near fp16's largest, and small ones."""
 import numpy as np
 import pytest
 import torch
@@ -106,6 +106,28 @@ def test_unbalanced_tokens(name, fmt):
     c = _cache(s, fmt, 4, fill=fill)
     for decode in (True, False):
         _check(lib, c, _q(s, 5), 1.0 / np.sqrt(s.dh), decode, floor=True)
+
+
+@pytest.mark.parametrize("decode", [True, False], ids=["decode", "prefill"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("a,b", [(240.0, 260.0), (2.0 ** 12, 15.0), (15.0, 2.0 ** 12)])
+def test_values_near_the_largest(a, b, name, fmt, decode):
+    """Rebuilt values just inside fp16's range (65504): right, and no error reported."""
+    lib, s = kpa(), SPLITS[name]
+    rng = np.random.default_rng(6)
+
+    def fill(plane, x, values):
+        if not values:
+            return
+        ea = s.h1 * s.d1
+        sign = rng.choice([-1.0, 1.0], x.shape)
+        x[:, :plane.a] = a * sign[:, :plane.a]
+        x[:, ea:plane.a] = 0.0                                     # one rank: the rebuilt sum is a b
+        x[:, plane.a:] = b * sign[:, plane.a:]
+
+    c = _cache(s, fmt, 7, fill=fill)
+    _check(lib, c, _q(s, 8), 1.0 / np.sqrt(s.dh), decode, floor=True)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
