@@ -6,9 +6,9 @@
 //   T_r[(i1,j1), s] = sum_j2 q[(i1,i2),(j1,j2)] B^K_r(s)[i2,j2]         (mma.sync m16n8k16)
 //   score[(i1,i2), s] = sum_r sum_j1 A^K_r(s)[i1,j1] T_r[(i1,j1), s]
 //   O_i2[(i1,j1), j2] += sum_{s,r} (p[(i1,i2), s] A^V_r(s)[i1,j1]) B^V_r(s)[i2,j2]
-// One warp takes 16 slots of one i2.  The query is exact in the operand type (bf16 over a
-// bf16 pool, fp16 over an e4m3 one, whose codes are exact in fp16), so the score products
-// run once.  p A^V is rounded once by 2^-11 relative: to tf32 over a bf16 pool, whose B^V goes
+// One warp takes 16 slots of one i2.  The query is an operand as it is over a bf16 pool, and over
+// an e4m3 one (whose codes are exact in fp16) fp16 times a power of two of the warp's own, so
+// the score products run once.  p A^V is rounded once by 2^-11 relative: to tf32 over a bf16 pool, whose B^V goes
 // into the product as it is (fp16 operands lose factors of ordinary products but unequal
 // magnitudes; they took 2 to 7 % less time: 8 x 4096 tokens of 4 x 8 heads of 8 x 16, R = 2,
 // 17.2 us against 18.6, 64 x 4096 102 against 106), to fp16 over an e4m3 one.  Sums, scores
@@ -164,10 +164,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t bf16x2_to_h2(uint32_t v) {
-    const float2 x = unpack_bf16x2(v);
-    return pack_h2(x.x, x.y);
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -295,8 +291,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                         f = ((2 * mt + (g >> 2)) * H2 + i2) * DH + (2 * (g & 3) + (v & 1)) * D2 + j2;
                     else
                         f = ((hs * MT + mt) * 16 + g + 8 * (v & 1)) * DH + j2;
-                    const uint32_t w = __ldg(qb + f / 2);
-                    qa[mt][ks][v] = Q8 ? bf16x2_to_h2(w) : w;
+                    qa[mt][ks][v] = __ldg(qb + f / 2);
+                }
+    }
+    // Over an e4m3 pool the query goes to fp16 times the power of two that takes the warp's largest
+    // element to [2^14, 2^15): exact to 2^-31 of that element, off by at most 2^-39 of it below.
+    float qscale = a.p.qscale;
+    if constexpr (Q8) {
+        uint32_t top = 0;                                  // the largest bits of a magnitude
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v)
+                    top = max(top, max(qa[mt][ks][v] & 0x7fffu, (qa[mt][ks][v] >> 16) & 0x7fffu));
+        top = __reduce_max_sync(0xffffffffu, top) >> 7;    // its exponent, biased by 127
+        const uint32_t up = min(268u - top, 253u);         // that of the power
+        const float scale = exp_byte(up);
+        qscale *= exp_byte(254u - up);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v) {
+                    const float2 x = fmul2(unpack_bf16x2(qa[mt][ks][v]), make_float2(scale, scale));
+                    qa[mt][ks][v] = pack_h2(x.x, x.y);
                 }
     }
     if (len < 0 || len > a.p.max_len) {
@@ -573,13 +594,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             // ---- scale and mask
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc) {
-                float2 ts[2] = {make_float2(a.p.qscale, a.p.qscale), make_float2(a.p.qscale, a.p.qscale)};
+                float2 ts[2] = {make_float2(qscale, qscale), make_float2(qscale, qscale)};
                 if constexpr (Q8) {
                     const unsigned char *e = smem + s * C::STAGE_BYTES + (gi0 + cc) * KG + C::EK * 16 + 4 * c;
                     const uint32_t s4 = exp_sum4(*reinterpret_cast<const uint32_t *>(e), *reinterpret_cast<const uint32_t *>(e + 16));
                     // bytes: slots 2c, 2c + 8, 2c + 1, 2c + 9
-                    ts[0] = make_float2(exp_sum(s4 & 255u) * a.p.qscale, exp_sum((s4 >> 16) & 255u) * a.p.qscale);
-                    ts[1] = make_float2(exp_sum((s4 >> 8) & 255u) * a.p.qscale, exp_sum(s4 >> 24) * a.p.qscale);
+                    ts[0] = make_float2(exp_sum(s4 & 255u) * qscale, exp_sum((s4 >> 16) & 255u) * qscale);
+                    ts[1] = make_float2(exp_sum((s4 >> 8) & 255u) * qscale, exp_sum(s4 >> 24) * qscale);
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)

@@ -429,8 +429,9 @@ kpa_status kpa_paged_prefill(const kpa_config *cfg, const kpa_pages *pages, int3
 
 /* The same attention for one token per sequence: the query is at position seq_len[b] - 1,
  * the newest slot.  The splits with a kernel of their own (kpa_paged_decode_kernel_kind)
- * never form K and V: scores are fp32 sums of exact products, and the weighted value
- * factors p A^V are rounded by 2^-11 relative: over a bf16 pool to tf32, with fp32's range;
+ * never form K and V: scores are fp32 sums of exact products (over an e4m3 pool, of query
+ * elements above 2^-31 of the sequence's largest; smaller ones are off by 2^-39 of that one),
+ * and the weighted value factors p A^V are rounded by 2^-11 relative: over a bf16 pool to tf32, with fp32's range;
  * over an e4m3 pool, the weights p first, to fp16, where a token's value factors keep that
  * precision while max |A| max |B| is in [2^-16, 2^22] (smaller ones lose it bit by bit; larger
  * ones may give outputs that are not finite, which is reported).

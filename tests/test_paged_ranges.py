@@ -1,5 +1,5 @@
 """Paged attention on the GPU over magnitudes, against the definition in 64 bits: factors whose A
-and B differ by powers of two, values near fp16's largest, and small ones."""
+and B differ by powers of two, values near fp16's largest, small ones, and queries far from 1."""
 import numpy as np
 import pytest
 import torch
@@ -151,3 +151,27 @@ def test_tiny_bf16_values(power, name):
         pytest.skip("the chunk kernels round a rebuilt value to fp16")
     c = _cache(s, "bf16", 11, scale_v=(2.0 ** power, 2.0 ** power))
     _check(lib, c, _q(s, 12), 1.0 / np.sqrt(s.dh), True, floor=False)
+
+
+@pytest.mark.parametrize("decode", [True, False], ids=["decode", "prefill"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("power", [-100, -20, 18, 100])
+def test_queries_far_from_one(power, name, fmt, decode):
+    """A query of any size whose scores are ordinary, as sm_scale takes its size back."""
+    lib, s = kpa(), SPLITS[name]
+    c = _cache(s, fmt, 13)
+    q = _q(s, 14, 0.3 * 2.0 ** power)
+    _check(lib, c, q, 4.0 / np.sqrt(s.dh) * 2.0 ** -power, decode, floor=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
+def test_query_elements_of_many_sizes(name, fmt):
+    """Elements of one query that differ by powers of two up to 2^16, and a head of zeros."""
+    lib, s = kpa(), SPLITS[name]
+    c = _cache(s, fmt, 15)
+    rng = np.random.default_rng(16)
+    q = _q(s, 17).double() * torch.from_numpy(np.exp2(rng.integers(-16, 1, (1, s.h, s.dh))))
+    q[0, s.h // 2] = 0
+    _check(lib, c, q.to(torch.bfloat16), 8.0 / np.sqrt(s.dh), True, floor=True)
