@@ -80,8 +80,9 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         const int64_t wave = (int64_t)sms * per_sm;
         // Long batches: the lengths, which are not known here, may differ, so the blocks size the splits (32
         // sequences of 1024 .. 8192 tokens, R = 4: 82 us, splits sized from the longest 91).  Short ones do
-        // not repay the search.
-        if (batch > 1 && batch <= kPagedMaxSlotSeqs && (per >= 16 || per_seq == 1) && tiles >= 8) {
+        // not repay the search.  (It sums the sequences' tiles in 32 bits.)
+        if (batch > 1 && batch <= kPagedMaxSlotSeqs && (per >= 16 || per_seq == 1) && tiles >= 8 &&
+            batch * tiles <= INT32_MAX) {
             p.n_slots = (int)(wave * std::min<int64_t>(4, (3 * (int64_t)batch + wave - 1) / wave));
             p.n_slots = std::max(p.n_slots, batch);
             p.n_split = 2;                                 // (partials, in slots)

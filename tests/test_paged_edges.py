@@ -49,6 +49,18 @@ def test_read_long_records(name, fmt):
         assert (x[:2] == 7).all() and (x[rows - 3:] == 7).all()
 
 
+def test_tiles_of_a_batch_past_32_bits():
+    """The blocks of a long batch size its parts from a 32-bit sum of tiles: a batch that may have
+    more (pages shared, so that it fits) takes one part a sequence, which needs no workspace."""
+    lib, page = kpa(), 4096
+    pages = lib.make_pages(page, 10, (1 << 19) - 1, "bf16")
+    for name in ("kpa_4x4_8x16_r2", "tpa_16_64_r2"):
+        cfg = lib.make_config(SPLITS[name], "bf16")
+        assert lib.kpa_paged_decode_workspace_size(cfg, pages, 200, 1 << 20) > 0
+        assert lib.kpa_paged_decode_workspace_size(cfg, pages, 256, page * ((1 << 19) - 1)) == 0
+        assert lib.kpa_paged_decode_workspace_size(cfg, pages, 256, page * ((1 << 19) - 1), 5000, 4) > 0
+
+
 TOP = 2 ** 31 - 1
 
 
