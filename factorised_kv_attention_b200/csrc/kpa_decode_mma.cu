@@ -546,8 +546,9 @@ decode_mma_kernel(DecodeArgs a, RopeTable rope, DecodeTestHooks hooks) {
 
     for (int t = 0; t < n_tiles; ++t) {
         const int s = t % STAGES;
-        if (!mbar_wait(full0 + 8 * s, (t / STAGES) & 1, limit)) {
-            raise_error(a.err, kErrTimeout);
+        // (a vote: a warp whose lanes differ, as the time runs out, must not part)
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, (t / STAGES) & 1, limit))) {
+            if (lane == 0) raise_error(a.err, kErrTimeout);
             flags[0] = 1;
             aborted = true;
             break;
@@ -778,7 +779,7 @@ decode_mma_kernel(DecodeArgs a, RopeTable rope, DecodeTestHooks hooks) {
                 flags[2] = t + STAGES + 1;
             }
         }
-        if (flags[0]) { aborted = true; break; }
+        if (__any_sync(0xffffffffu, flags[0])) { aborted = true; break; }
     }
 
     {   // fp16 operands of the value product: an out-of-range value makes the partial non-finite
@@ -868,8 +869,9 @@ decode_mma_kernel(DecodeArgs a, RopeTable rope, DecodeTestHooks hooks) {
 
     for (int t = 0; t < n_tiles; ++t) {
         const int s = t % STAGES;
-        if (!mbar_wait(full0 + 8 * s, (t / STAGES) & 1, limit)) {
-            raise_error(a.err, kErrTimeout);
+        // (a vote: a warp whose lanes differ, as the time runs out, must not part)
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, (t / STAGES) & 1, limit))) {
+            if (lane == 0) raise_error(a.err, kErrTimeout);
             flags[0] = 1;
             aborted = true;
             break;
@@ -1174,7 +1176,7 @@ decode_mma_kernel(DecodeArgs a, RopeTable rope, DecodeTestHooks hooks) {
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * s);
-        if (flags[0]) { aborted = true; break; }
+        if (__any_sync(0xffffffffu, flags[0])) { aborted = true; break; }
     }
 
     if constexpr (C::ORDER3) {
