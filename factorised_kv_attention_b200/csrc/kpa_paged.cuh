@@ -28,8 +28,8 @@ __device__ __forceinline__ void split_group(const Pool &p, int g, int &entry, in
     in = g - entry * p.pg;
 }
 
-// Which slots a row at position pos sees: [0, sinks) and [pos - window + 1, pos].  lo is the
-// start of the window for the first (smallest) position of a set of rows.
+// Which slots a row at position pos sees: every one up to pos without a window, else [0, sinks)
+// and [pos - window + 1, pos].
 struct Mask {
     int window, sinks;
 };
@@ -242,7 +242,8 @@ __device__ __forceinline__ uint32_t exp_sum4(uint32_t a4, uint32_t b4) {
     const uint32_t t = ((a4 & 0x7f7f7f7fu) + (b4 & 0x7f7f7f7fu)) ^ ((a4 ^ b4) & 0x80808080u);
     return ((t & 0x7f7f7f7fu) + 0x02020202u) ^ (~t & 0x80808080u);          // + 130 = - 126
 }
-// 2^(byte - 128), byte in [0, 254]: half of 2^(byte - 127) (byte 0: 2^-128 as a denormal)
+// 2^(byte - 128), byte in [1, 254]: half of 2^(byte - 127).  0 for byte 0, where both exponents are
+// the smallest that are written, -64: products below 2^-110.
 __device__ __forceinline__ float exp_sum(uint32_t byte) { return 0.5f * __uint_as_float(byte << 23); }
 
 }  // namespace paged

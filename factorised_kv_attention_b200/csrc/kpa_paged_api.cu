@@ -95,7 +95,8 @@ AttnPlan plan_attn(const PagedShape &ps, int batch, int n_rows, bool chunks, int
         // A sequence's splits merge in one cluster, without a second kernel, where every CTA is resident at
         // once (a cluster holds its SMs until its longest split ends) and the splits get no more than two
         // tiles or a quarter longer for it: the second kernel and its launch cost about as much (8 x 4096
-        // tokens, 16 heads of 64: 10.9 us on the device and 6.6 of the host against 9.7 and 12.4).
+        // tokens of 16 heads of 64, bf16: 10.7 us in a replayed graph and 6.2 of the host against 10.0 and 8.2;
+        // 64 x 4096 of 32 heads of 64, e4m3: 25.1 and 6.0 against 26.7 and 8.0).
         const int64_t most = std::min<int64_t>(kPagedMaxCluster, (int64_t)sms * per_sm / batch);
         for (int64_t t = per; t <= std::max(per + 2, per + per / 4) && most > 1; ++t) {
             const int64_t n = (tiles + t - 1) / t;

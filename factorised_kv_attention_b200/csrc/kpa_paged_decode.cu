@@ -28,9 +28,9 @@
 // query does not see are masked in the scores and zeroed in the value operands, so their
 // bytes may hold anything.  Waits are bounded.
 //
-// Bound by instructions: 2^19 tokens of 4 x 8 heads of 8 x 16, R = 2, in e4m3 in 152 us (2.2 TB/s,
-// 66 % of the issue slots); 32 ragged sequences at R = 4 in bf16 in 82 us (3.8 TB/s); by latency on
-// short ones: 8 x 4096 tokens of 16 heads of 64 in 11 us.
+// Bound by instructions: 2^19 tokens of 4 x 8 heads of 8 x 16, R = 2, in e4m3 in 156 us (2.2 TB/s,
+// 67 % of the issue slots); 32 ragged sequences at R = 4 in bf16 in 87 us (3.6 TB/s; tensor pipe
+// 32 %); by latency on short ones: 8 x 4096 tokens of 16 heads of 64 in 11.6 us.
 #include "kpa_f32x2.cuh"
 #include "kpa_paged.cuh"
 #include "kpa_sm100.cuh"
@@ -739,50 +739,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                                     for (int mt = 0; mt < MT; ++mt) mma_tf32(o[mt][n0 + k], pt[hf][mt], b0, b1);
                                 }
                         }
-                        continue;
-                    }
-                    uint32_t pa[MT][4];                            // P' = p A^V_r: (half, rows g / g + 8)
+                    } else {
+                        uint32_t pa[MT][4];                            // P' = p A^V_r: (half, rows g / g + 8)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int rh = 0; rh < 2; ++rh) {
-                            const int j = (r * MT + mt) * 2 + rh, hr = KPA ? 0 : rh;
-                            uint32_t lo, hi;
-                            e4m3_split(ew[0][j], lo, hi);
-                            pa[mt][rh] = hmul2(p2[mt][hr][0], lo);
-                            pa[mt][2 + rh] = hmul2(p2[mt][hr][1], hi);
-                            if constexpr (MASKED) {
-                                pa[mt][rh] = mask_pair(pa[mt][rh], keep[0][0], keep[0][1]);
-                                pa[mt][2 + rh] = mask_pair(pa[mt][2 + rh], keep[1][0], keep[1][1]);
+                            for (int rh = 0; rh < 2; ++rh) {
+                                const int j = (r * MT + mt) * 2 + rh, hr = KPA ? 0 : rh;
+                                uint32_t lo, hi;
+                                e4m3_split(ew[0][j], lo, hi);
+                                pa[mt][rh] = hmul2(p2[mt][hr][0], lo);
+                                pa[mt][2 + rh] = hmul2(p2[mt][hr][1], hi);
+                                if constexpr (MASKED) {
+                                    pa[mt][rh] = mask_pair(pa[mt][rh], keep[0][0], keep[0][1]);
+                                    pa[mt][2 + rh] = mask_pair(pa[mt][2 + rh], keep[1][0], keep[1][1]);
+                                }
                             }
-                        }
-                    constexpr int STEP = NT >= 4 ? 4 : 2;          // 8-feature blocks per load
+                        constexpr int STEP = NT >= 4 ? 4 : 2;          // 8-feature blocks per load
 #pragma unroll
-                    for (int n0 = 0; n0 < NT; n0 += STEP) {
-                        uint32_t b0[STEP], b1[STEP];
-                        uint32_t bw[STEP];
-                        ldsm_list<STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
-                            return b_row(r * NT + (NT == 1 ? 0 : n0 + j));
-                        });
-#pragma unroll
-                        for (int k = 0; k < STEP; ++k) {
-                            e4m3_split(bw[k], b0[k], b1[k]);
-                            b0[k] = hmul2(b0[k], vs[0]);
-                            b1[k] = hmul2(b1[k], vs[1]);
-                        }
-                        if constexpr (MASKED) {
+                        for (int n0 = 0; n0 < NT; n0 += STEP) {
+                            uint32_t b0[STEP], b1[STEP];
+                            uint32_t bw[STEP];
+                            ldsm_list<STEP, false>(vgrp + A_V * 16, lane, bw, [&](int j) {
+                                return b_row(r * NT + (NT == 1 ? 0 : n0 + j));
+                            });
 #pragma unroll
                             for (int k = 0; k < STEP; ++k) {
-                                b0[k] = mask_pair(b0[k], keep[0][0], keep[0][1]);
-                                b1[k] = mask_pair(b1[k], keep[1][0], keep[1][1]);
+                                e4m3_split(bw[k], b0[k], b1[k]);
+                                b0[k] = hmul2(b0[k], vs[0]);
+                                b1[k] = hmul2(b1[k], vs[1]);
                             }
+                            if constexpr (MASKED) {
+#pragma unroll
+                                for (int k = 0; k < STEP; ++k) {
+                                    b0[k] = mask_pair(b0[k], keep[0][0], keep[0][1]);
+                                    b1[k] = mask_pair(b1[k], keep[1][0], keep[1][1]);
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < STEP; ++k)
+                                if (n0 + k < NT) {
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt) mma16<true>(o[mt][n0 + k < NT ? n0 + k : 0], pa[mt], b0[k], b1[k]);
+                                }
                         }
-#pragma unroll
-                        for (int k = 0; k < STEP; ++k)
-                            if (n0 + k < NT) {
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) mma16<true>(o[mt][n0 + k < NT ? n0 + k : 0], pa[mt], b0[k], b1[k]);
-                            }
                     }
                 }
             }
@@ -912,11 +912,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     if (a.cluster) join_cluster();
 }
 
-// (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools).
+// (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools): the
+// head splits of this repository's decode workloads whose i2 share the 16 warps of an SM evenly (h2
+// a power of two) and whose h1 d1 is a multiple of 16.  h2 of 5 and 10 and h = 61 would need slices and padding of their own; they run on the chunk
+// kernel, at its pace (4 x 5 heads of 8 x 8, R = 2, 8 x 4096 tokens: 275 us; 4 x 4 heads here: 15).
 // Blocks are as large as an SM holds: smaller ones start sooner on short sequences and lose more on long
-// ones (variant 0, bf16, 4 slices and 3 stages against 8 and 2: 8 x 4096 tokens 9.9 us against 11.2,
-// 64 x 4096 51 against 45, 4 x 65536 55 against 35; variant 4, e4m3, 2 slices of 4 chunks against 8 of 2:
-// 64 x 4096 25.2 against 24.7, 65536 36.9 against 16.8).
+// ones (variant 0, bf16, 4 slices and 3 stages against 8 and 2: 8 x 4096 tokens 9.9 us against 10.7,
+// 64 x 4096 53 against 45, 4 x 65536 57 against 35; variant 4, e4m3, 2 slices of 4 chunks against 8 of 2:
+// 64 x 4096 25.8 against 25.1, 65536 37.3 against 16.7).
 #define KPA_PAGED_DECODE_VARIANTS(X)            \
     X(0, 16, 1, 64, 2, 2, 1, 1, 8, 1, 2, 8, 2, 2)    \
     X(1, 32, 8, 16, 4, 4, 8, 1, 2, 1, 2, 2, 2, 2)    \

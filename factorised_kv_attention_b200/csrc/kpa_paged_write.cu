@@ -40,7 +40,7 @@ struct WriteArgs {
     int *err;
 };
 
-// 16-slot groups that the rows of sequence b touch.
+// a / 16 rounded down, positions below 0 too
 __device__ __forceinline__ long long floor16(long long a) { return a >= 0 ? a / 16 : -((-a + 15) / 16); }
 
 // byte of slot t inside a row of an e4m3 group

@@ -358,7 +358,8 @@ kpa_status kpa_append(const kpa_config *cfg, int32_t batch, int32_t n_tok, const
  * no rows.  Rows of no sequence (before cu_rows[0], or at and behind cu_rows[batch]) are
  * neither read nor written.  A sequence whose cu_rows descend or leave [0, n_rows] sets
  * KPA_ERR_DEVICE_CHECK and is skipped (an attention may leave unspecified values in the
- * rows of `out` that it names).
+ * rows of `out` that it names; where other sequences' rows overlap because of it, some of those
+ * may not be computed).
  *
  * Page table entries are looked at only for slots that the call writes or that some of its
  * rows see; the others may hold anything.  An entry outside [0, n_pages) sets
@@ -410,7 +411,9 @@ kpa_status kpa_paged_read_factors(const kpa_config *cfg, const kpa_pages *pages,
  *        no initialisation and holds nothing between calls.  Calls that may run at the same
  *        time need workspaces of their own.
  * K and V are rebuilt from the factors on chip and rounded once to fp16, as are the scaled
- * query and the softmax weights; products accumulate in fp32, and the softmax is fp32.  A
+ * query and the softmax weights: each is off by 2^-11 of itself, or by 2^-25 where that is more
+ * (rebuilt sums below 2^-14 lose precision bit by bit, those below 2^-25 are taken as 0);
+ * products accumulate in fp32, and the softmax is fp32.  A
  * cached value that is not finite, or a rebuilt one outside fp16's range, leaves the rows
  * that see it, and possibly other rows of the same sequence and call, unspecified; outputs
  * that are not finite set KPA_ERR_DEVICE_CHECK.  Slots that none of the sequence's rows
