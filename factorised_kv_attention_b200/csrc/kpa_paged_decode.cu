@@ -294,32 +294,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                     qa[mt][ks][v] = __ldg(qb + f / 2);
                 }
     }
-    // Over an e4m3 pool the query goes to fp16 times the power of two that takes the warp's largest
-    // element to [2^14, 2^15): exact to 2^-31 of that element, off by at most 2^-39 of it below.
-    float qscale = a.p.qscale;
-    if constexpr (Q8) {
-        uint32_t top = 0;                                  // the largest bits of a magnitude
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v)
-                    top = max(top, max(qa[mt][ks][v] & 0x7fffu, (qa[mt][ks][v] >> 16) & 0x7fffu));
-        top = __reduce_max_sync(0xffffffffu, top) >> 7;    // its exponent, biased by 127
-        const uint32_t up = min(268u - top, 253u);         // that of the power
-        const float scale = exp_byte(up);
-        qscale *= exp_byte(254u - up);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v) {
-                    const float2 x = fmul2(unpack_bf16x2(qa[mt][ks][v]), make_float2(scale, scale));
-                    qa[mt][ks][v] = pack_h2(x.x, x.y);
-                }
-    }
     if (len < 0 || len > a.p.max_len) {
         if (split == 0 && tid == 0) raise_error(a.p.err, kErrDeviceCheck);
         len = len < 0 ? 0 : a.p.max_len;
@@ -423,6 +397,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         copy_groups(i / TG, i % TG, has, has ? group_index(first_page, first_in) : 0);
     }
 
+    // Over an e4m3 pool the query goes to fp16 times the power of two that takes the warp's largest
+    // finite element to [2^14, 2^15): exact to 2^-31 of that element, off by at most 2^-39 of it below.  (Here: the first copies are on their way.)
+    float qscale = a.p.qscale;
+    if constexpr (Q8) {
+        auto largest = [&](uint32_t limit) {               // largest bits of a magnitude up to limit
+            uint32_t top = 0;
+            auto take = [&](uint32_t bits) { top = max(top, bits <= limit ? bits : 0u); };
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v) {
+                        take(qa[mt][ks][v] & 0x7fffu);
+                        take((qa[mt][ks][v] >> 16) & 0x7fffu);
+                    }
+            return __reduce_max_sync(0xffffffffu, top);
+        };
+        uint32_t top = largest(0x7fffu);
+        if (top >= 0x7f80u) top = largest(0x7f7fu);        // (an element is not finite)
+        top >>= 7;                                         // its exponent, biased by 127
+        const uint32_t up = min(268u - top, 253u);         // that of the power
+        const float scale = exp_byte(up);
+        qscale *= exp_byte(254u - up);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < (D2 == 8 ? 2 : 4); ++v) {
+                    const float2 x = fmul2(unpack_bf16x2(qa[mt][ks][v]), make_float2(scale, scale));
+                    qa[mt][ks][v] = pack_h2(x.x, x.y);
+                }
+    }
     float o[MT][NT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)

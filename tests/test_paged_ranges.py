@@ -175,3 +175,19 @@ def test_query_elements_of_many_sizes(name, fmt):
     q = _q(s, 17).double() * torch.from_numpy(np.exp2(rng.integers(-16, 1, (1, s.h, s.dh))))
     q[0, s.h // 2] = 0
     _check(lib, c, q.to(torch.bfloat16), 8.0 / np.sqrt(s.dh), True, floor=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_bad_query_element_stays_in_its_head(bad, name, fmt):
+    """A query element that is not finite: reported, and the other heads are right."""
+    lib, s = kpa(), SPLITS[name]
+    c = _cache(s, fmt, 18)
+    q, scale = _q(s, 19), 4.0 / np.sqrt(s.dh)
+    want, tol, _ = pm.attention(q, [N - 1], *pm.planes(c, 0, N, "cpu"), 0, 0, scale)
+    q[0, 1, 3] = bad
+    for decode in (True, False):
+        got = _attend(lib, c, q, scale, decode, lib.KPA_ERR_DEVICE_CHECK)
+        rest = [h for h in range(s.h) if h != 1]
+        pu.assert_within(got[:, rest], want[:, rest].numpy(), tol[:, rest].numpy(), "decode" if decode else "prefill")
