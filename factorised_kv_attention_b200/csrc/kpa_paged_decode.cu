@@ -151,7 +151,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// a float whose upper 19 bits, which a tf32 operand is, are x rounded to nearest (2^-11 relative)
+// a float whose upper 19 bits, which a tf32 operand is, are x rounded to nearest (2^-11 relative); a NaN
+// does not stay one (conversions that keep it take 7 to 17 % of the kernel)
 __device__ __forceinline__ uint32_t to_tf32(float x) { return __float_as_uint(x) + 0x1000u; }
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -169,6 +170,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// max as two bf16s, NaN where either is
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm volatile("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t mask_pair(uint32_t v, bool k0, bool k1) {
     return (k0 ? (v & 0xffffu) : 0u) | (k1 ? (v & 0xffff0000u) : 0u);
 }
@@ -180,6 +187,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
     constexpr int TG = C::TG, STAGES = C::STAGES, WARPS = C::WARPS, CHUNKS = C::CHUNKS, SLICES = C::SLICES, HS = C::HS;
     constexpr int KG = C::KG, VG = C::VG, A_K = RK * MA, A_V = RV * MA;
     constexpr bool Q8 = C::Q8, KPA = C::KPA;
+    [[maybe_unused]] constexpr bool TURNS = H2 >= 4;       // (bf16) the warps of a slice share the look for NaN
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t full0 = smem_u32(smem + C::OFF_BARS);
     size_t *tab = reinterpret_cast<size_t *>(smem + C::OFF_TAB);
@@ -444,6 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
             m_run[mt][hr] = -INFINITY;
             l_run[mt][hr] = 0.f;
         }
+    uint32_t top_av = 0;                                   // the largest bf16 A^V of this thread, or NaN (which products lose)
     bool aborted = false;
 
     // rows (16 bytes each) of matrix j's fragments inside a group
@@ -710,6 +719,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
                         ldsm_list<RV * 2 * MT, false>(vgrp + hf * (C::EV * 16), lane, ew[hf], a_row);
+                    // Is an A^V a NaN?  The h2 warps of a slice hold the same ones: with four and more, each looks
+                    // at its share (all of them by every warp: 4 % of the kernel at R = 4, the shares 1 %).
+                    if constexpr (TURNS) {
+                        constexpr int ALL = RV * 2 * MT, SHARE = 2 * ALL / H2, N = SHARE < 2 ? 2 : SHARE;
+                        uint32_t w[N];
+                        auto place = [&](int k) { return (i2 * SHARE + k) % (2 * ALL); };
+                        ldsm_list<N, false>(vgrp, lane, w, [&](int k) { return a_row(place(k) % ALL) + place(k) / ALL * C::EV; });
+#pragma unroll
+                        for (int k = 0; k < N; ++k) {
+                            const bool hf = place(k) >= ALL;
+                            if constexpr (MASKED) w[k] = mask_pair(w[k], hf ? keep[1][0] : keep[0][0], hf ? keep[1][1] : keep[0][1]);
+                            top_av = max_nan_bf16x2(top_av, w[k]);
+                        }
+                    } else if constexpr (MASKED) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int j = 0; j < RV * 2 * MT; ++j) {
+                                ew[hf][j] = mask_pair(ew[hf][j], keep[hf][0], keep[hf][1]);
+                                top_av = max_nan_bf16x2(top_av, ew[hf][j]);
+                            }
+                    }
                 }
 #pragma unroll
                 for (int r = 0; r < RV; ++r) {
@@ -724,9 +755,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
                             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                                 for (int rh = 0; rh < 2; ++rh) {
-                                    const float2 x = fmul2(sc[cc][mt][KPA ? 0 : rh][hf], unpack_bf16x2(ew[hf][(r * MT + mt) * 2 + rh]));
-                                    pt[hf][mt][rh] = !MASKED || keep[hf][0] ? to_tf32(x.x) : 0u;
-                                    pt[hf][mt][2 + rh] = !MASKED || keep[hf][1] ? to_tf32(x.y) : 0u;
+                                    const uint32_t w = ew[hf][(r * MT + mt) * 2 + rh];
+                                    if constexpr (!MASKED && !TURNS) top_av = max_nan_bf16x2(top_av, w);
+                                    const float2 x = fmul2(sc[cc][mt][KPA ? 0 : rh][hf], unpack_bf16x2(w));
+                                    pt[hf][mt][rh] = !MASKED || !TURNS || keep[hf][0] ? to_tf32(x.x) : 0u;
+                                    pt[hf][mt][2 + rh] = !MASKED || !TURNS || keep[hf][1] ? to_tf32(x.y) : 0u;
                                 }
                         constexpr int STEP = NT >= 2 ? 2 : 1;          // 8-feature blocks per load
 #pragma unroll
@@ -877,7 +910,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
         }
     __syncthreads();
     constexpr float kBack = Q8 ? 1.f / 256.f : 1.f;
-    bool finite = true;
+    bool finite = (top_av & 0x7fffu) <= 0x7f80u && (top_av >> 16 & 0x7fffu) <= 0x7f80u;
     for (int i4 = tid; i4 < H * DH / 4; i4 += C::THREADS) {
         const int head = i4 * 4 / DH, col = i4 * 4 % DH;
         float M = -INFINITY;

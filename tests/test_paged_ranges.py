@@ -191,3 +191,22 @@ def test_a_bad_query_element_stays_in_its_head(bad, name, fmt):
         got = _attend(lib, c, q, scale, decode, lib.KPA_ERR_DEVICE_CHECK)
         rest = [h for h in range(s.h) if h != 1]
         pu.assert_within(got[:, rest], want[:, rest].numpy(), tol[:, rest].numpy(), "decode" if decode else "prefill")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("plane", ["v"])
+@pytest.mark.parametrize("part", ["A", "B"])
+def test_a_bad_value_of_any_slot_is_reported(part, plane, name, fmt):
+    """A NaN in any place of a 16-slot group, in the first factor or the last, and an infinity among
+    the values (a key's may give a score of -inf, whose weight is 0)."""
+    lib, s = kpa(), SPLITS[name]
+    q, scale = _q(s, 20), 1.0 / np.sqrt(s.dh)
+    for slot in range(13, 34):
+        def fill(p, x, values):
+            if values == (plane == "v"):
+                bad = np.nan if plane == "k" or slot % 2 else (np.inf if slot % 3 else -np.inf)
+                x[slot, p.a - 1 if part == "A" else p.a] = bad
+        c = _cache(s, fmt, 21, fill=fill)
+        for decode in (True, False):
+            _attend(lib, c, q, scale, decode, lib.KPA_ERR_DEVICE_CHECK)
