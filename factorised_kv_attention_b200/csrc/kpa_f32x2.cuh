@@ -64,12 +64,13 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 // fit on [-1/2, 1/2] reweighted toward equal relative ripple; that script also
 // evaluates this exact float32 sequence over [-126, 8] (maximum relative error 2.7e-6).
 // x is clamped at -126 so the scaled result stays representable (it is then ~1e-38).
+// A NaN is not clamped: its result lies beyond fp16's range, and is infinite once rounded to it.
 __device__ __forceinline__ float2 exp2_poly2(float2 x) {
     constexpr float kRound = 12582912.f;            // 1.5 * 2^23: x + kRound holds round(x) in its low bits
     constexpr float c0 = 0x1.ffffe8p-1f, c1 = 0x1.62e0dep-1f, c2 = 0x1.ec06dap-3f, c3 = 0x1.ca13f8p-5f,
                     c4 = 0x1.399750p-7f;
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));          // -126, or NaN
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
     const float2 j = fadd2(x, make_float2(kRound, kRound));
     const float2 f = fsub2(x, fsub2(j, make_float2(kRound, kRound)));
     float2 p = ffma2(make_float2(c4, c4), f, make_float2(c3, c3));

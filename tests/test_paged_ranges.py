@@ -195,7 +195,7 @@ def test_a_bad_query_element_stays_in_its_head(bad, name, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("name", NAMES)
-@pytest.mark.parametrize("plane", ["v"])
+@pytest.mark.parametrize("plane", ["k", "v"])
 @pytest.mark.parametrize("part", ["A", "B"])
 def test_a_bad_value_of_any_slot_is_reported(part, plane, name, fmt):
     """A NaN in any place of a 16-slot group, in the first factor or the last, and an infinity among
@@ -210,3 +210,13 @@ def test_a_bad_value_of_any_slot_is_reported(part, plane, name, fmt):
         c = _cache(s, fmt, 21, fill=fill)
         for decode in (True, False):
             _attend(lib, c, q, scale, decode, lib.KPA_ERR_DEVICE_CHECK)
+
+
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -0x400000, -1], ids=hex)
+def test_the_polynomial_exponential_of_a_nan_is_no_fp16(bits):
+    """So a score that is NaN does not give a weight of 0."""
+    lib = kpa()
+    x = torch.tensor([bits] * 4, dtype=torch.int32, device="cuda").view(torch.float32)
+    y = torch.zeros_like(x)
+    lib.kpa_test_exp2_poly(x, y)
+    assert not y.to(torch.float16).isfinite().any()
