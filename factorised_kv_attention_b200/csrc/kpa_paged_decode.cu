@@ -10,8 +10,8 @@
 // an e4m3 one (whose codes are exact in fp16) fp16 times a power of two of the warp's own, so
 // the score products run once.  p A^V is rounded once by 2^-11 relative: to tf32 over a bf16 pool, whose B^V goes
 // into the product as it is (fp16 operands lose factors of ordinary products but unequal
-// magnitudes; they took 2 to 7 % less time: 8 x 4096 tokens of 4 x 8 heads of 8 x 16, R = 2,
-// 17.2 us against 18.6, 64 x 4096 102 against 106), to fp16 over an e4m3 one.  Sums, scores
+// magnitudes; they took 1 to 6 % less time: 8 x 4096 tokens of 4 x 8 heads of 8 x 16, R = 2,
+// 17.2 us against 18.2, 64 x 4096 102 against 107), to fp16 over an e4m3 one.  Sums, scores
 // and the softmax are fp32.  With d1 = 8 the rows of an m-tile pair up two j1 of one head per lane, so the
 // sum over j1 is one add and two shuffles; with d1 = 1 (TPA) rows are heads.
 //
@@ -28,9 +28,9 @@
 // query does not see are masked in the scores and zeroed in the value operands, so their
 // bytes may hold anything.  Waits are bounded.
 //
-// Bound by instructions: 2^19 tokens of 4 x 8 heads of 8 x 16, R = 2, in e4m3 in 156 us (2.2 TB/s,
+// Bound by instructions: 2^19 tokens of 4 x 8 heads of 8 x 16, R = 2, in e4m3 in 155 us (2.2 TB/s,
 // 67 % of the issue slots); 32 ragged sequences at R = 4 in bf16 in 87 us (3.6 TB/s; tensor pipe
-// 32 %); by latency on short ones: 8 x 4096 tokens of 16 heads of 64 in 11.6 us.
+// 32 %); by latency on short ones: 8 x 4096 tokens of 16 heads of 64 in 11.7 us.
 #include "kpa_f32x2.cuh"
 #include "kpa_paged.cuh"
 #include "kpa_sm100.cuh"
@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_kernel(const Decod
 // (variant, MA, D1, D2, RK, RV, H2, HS, then SLICES, CHUNKS, STAGES for bf16 and for e4m3 pools): the
 // head splits of this repository's decode workloads whose i2 share the 16 warps of an SM evenly (h2
 // a power of two) and whose h1 d1 is a multiple of 16.  h2 of 5 and 10 and h = 61 would need slices and padding of their own; they run on the chunk
-// kernel, at its pace (4 x 5 heads of 8 x 8, R = 2, 8 x 4096 tokens: 275 us; 4 x 4 heads here: 15).
+// kernel, at its pace (4 x 5 heads of 8 x 8, R = 2, 8 x 4096 tokens: 275 us; 4 x 4 heads here: 16).
 // Blocks are as large as an SM holds: smaller ones start sooner on short sequences and lose more on long
 // ones (variant 0, bf16, 4 slices and 3 stages against 8 and 2: 8 x 4096 tokens 9.9 us against 10.7,
 // 64 x 4096 53 against 45, 4 x 65536 57 against 35; variant 4, e4m3, 2 slices of 4 chunks against 8 of 2:
